@@ -84,7 +84,7 @@ typedef enum {
 #define MOE_QUANT_ROW 1 /* quantise along the last axis (cols) */
 #define MOE_QUANT_COL 2 /* quantise along rows, store transposed */
 
-/* Element types of moe_router_topk's logits. */
+/* Element types (router logits, sources and results of the MXFP4 calls). */
 #define MOE_DTYPE_F32 0
 #define MOE_DTYPE_BF16 1
 
@@ -96,6 +96,8 @@ typedef enum {
 #define MOE_OP_FWD_FP8_TENSOR 5
 #define MOE_OP_BWD_BF16 6
 #define MOE_OP_BWD_FP8_TENSOR 7
+#define MOE_OP_ROUTER_LOSSES 8
+#define MOE_OP_FWD_MXFP4 9
 
 /* Limits checked on the host. */
 #define MOE_MAX_EXPERTS 256
@@ -112,7 +114,8 @@ int64_t moe_mx_scale_bytes(int32_t groups, int64_t rows, int64_t k);
 int64_t moe_padded_rows(int32_t T, int32_t k, int32_t E);
 
 /* Workspace bytes for op MOE_OP_PERMUTE / MOE_OP_FWD / MOE_OP_BWD /
- * MOE_OP_FWD_BF16 / MOE_OP_FWD_FP8_TENSOR / MOE_OP_BWD_BF16 / MOE_OP_BWD_FP8_TENSOR of a layer
+ * MOE_OP_FWD_BF16 / MOE_OP_FWD_FP8_TENSOR / MOE_OP_BWD_BF16 / MOE_OP_BWD_FP8_TENSOR /
+ * MOE_OP_ROUTER_LOSSES (H and I not used) / MOE_OP_FWD_MXFP4 of a layer
  * (T tokens, top-k, E experts, hidden H, intermediate I).  -1 if invalid. */
 int64_t moe_workspace_size(int32_t op, int32_t T, int32_t k, int32_t E, int32_t H, int32_t I);
 
@@ -402,6 +405,99 @@ moe_status_t moe_route_permute(const void* logits, int32_t logits_dtype, const v
                                int32_t* split_sizes, int32_t* group_offsets, int32_t* row_to_slot,
                                int32_t* slot_to_row, float* prob_perm, uint8_t* xq, uint8_t* xq_sf, uint8_t* xq_col,
                                uint8_t* xq_col_sf, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* Router for training: what moe_router_topk computes, and from the same read
+ * of the logits the tokens per expert, the load-balance loss and the z-loss.
+ * With z the logits of a token, s = softmax(z) over all E experts, lse =
+ * log sum_e exp(z_e) and n the number of unmasked tokens:
+ *   counts[e]    = kept slots of unmasked tokens on expert e
+ *   prob_sums[e] = sum over unmasked tokens of s_e
+ *   losses[0]    = E * sum_e (counts[e] / (n k)) * (prob_sums[e] / n)   (1 when balanced)
+ *   losses[1]    = (1 / n) * sum over unmasked tokens of lse^2
+ *   (n == 0: both 0).
+ * The pages name no such losses (Challenge 1 shows only that the groups' sizes
+ * are the router's); these are the usual definitions, unscaled.
+ *   token_mask  NULL, or [T] bytes: 0 marks padding.  A masked token gets ids
+ *               like any other (the layer's shapes stay) but probabilities 0
+ *               and lse 0, and nothing of its logits counts, NaN included.
+ *   topk_idx    int32 [T][k], as moe_router_topk;
+ *   topk_prob   float [T][k], as moe_router_topk up to fp32 rounding (the
+ *               sum over the kept experts runs in descending order here).
+ *   lse         float [T]; counts int32 [E]; prob_sums float [E]; tokens
+ *               int32 [1] = n; losses float [2].
+ *   workspace   >= moe_workspace_size(MOE_OP_ROUTER_LOSSES, T, k, E, 0, 0).
+ * NaN logits rank as -inf in the selection; an unmasked token with a NaN or
+ * +inf logit, or with all of them -inf, makes the losses NaN.  Sums run in a
+ * fixed order (the same inputs give the same bits).
+ * E <= MOE_MAX_EXPERTS, k <= min(E, 32), T*k < 2^30; arrays aligned to their
+ * elements, the workspace to 16 bytes. */
+moe_status_t moe_router_losses(const void* logits, int32_t logits_dtype, int32_t T, int32_t E, int32_t k,
+                               const uint8_t* token_mask, int32_t* topk_idx, float* topk_prob, float* lse,
+                               int32_t* counts, float* prob_sums, int32_t* tokens, float* losses, void* workspace,
+                               size_t workspace_bytes, moe_stream_t stream);
+
+/* Gradient of the logits, after moe_router_losses on the same logits and mask:
+ * through the kept probabilities (dprob, e.g. from a moe_grouped_mlp_bwd*
+ * call) and through the two losses (dlosses; the counts carry no gradient):
+ *   dz_e = dlosses[0] (E/n) s_e (f_e - sum_j f_j s_j) + dlosses[1] (2/n) lse s_e
+ *        + sum_{i: idx_i = e} p_i (dprob_i - sum_j p_j dprob_j),  f_e = counts[e] / (n k)
+ * and 0 for masked tokens.
+ *   counts, tokens  of moe_router_losses, or their sums over the ranks of a
+ *                   data-parallel job (both, for a loss over the whole batch).
+ *   dprob           float [T][k], or NULL for none.
+ *   dlosses         device float [2], or NULL for none.
+ *   dlogits         [T][E], the logits' type (fp32 arithmetic, one rounding).
+ * An id outside [0, E) in topk_idx is recorded as MOE_ERR_DEVICE_INDEX and left
+ * out; one that a token lists twice gets both gradients.  Limits as
+ * moe_router_losses. */
+moe_status_t moe_router_bwd(const void* logits, int32_t logits_dtype, int32_t T, int32_t E, int32_t k,
+                            const uint8_t* token_mask, const int32_t* topk_idx, const float* topk_prob,
+                            const float* lse, const int32_t* counts, const int32_t* tokens, const float* dprob,
+                            const float* dlosses, void* dlogits, moe_stream_t stream);
+
+/* ------------------------------------------------------------- MXFP4 --- */
+
+/* MXFP4 quantisation: as MXFP8 (one E8M0 scale per 32 consecutive values along
+ * the last axis, the same blocked scale layout, moe_mx_scale_bytes) with
+ * 4-bit E2M1 elements: +-{0, .5, 1, 1.5, 2, 3, 4, 6}.
+ *   src   [groups][rows][cols] bf16 or fp32 (dtype), contiguous.
+ *   q     uint8 [groups][rows][cols/2]: element 2i in the low four bits of byte
+ *         i, element 2i+1 in the high four.
+ *   sf    blocked scales (groups, rows, cols); bytes of no block are 0.
+ * Scale rule: s = smallest integer with amax/2^s <= 6, clamped to [-127, 127];
+ * all-zero block -> s = -127; block with NaN/Inf -> scale byte 0xFF (its codes
+ * say nothing).  Codes: E2M1(v * 2^-s), round to nearest even.
+ * Needs cols % 32 == 0 and groups*rows*cols < 2^34 - 2^27 (MOE_ERR_UNSUPPORTED
+ * otherwise), pointers 16-byte aligned.  Codes in rows order and scales in
+ * plain order from elsewhere (a checkpoint in 4 bits) are taken as they are,
+ * the scales after moe_mx_scales_to_blocked. */
+moe_status_t moe_mlp_quantize_mxfp4(const void* src, int32_t dtype, int32_t groups, int64_t rows, int64_t cols,
+                                    uint8_t* q, uint8_t* sf, moe_stream_t stream);
+
+/* The values that codes and scales stand for: dst [groups][rows][cols], bf16 or
+ * fp32 (dtype), code * 2^(b - 127), NaN for scale byte 0xFF; exact in both
+ * types, but for values past them: a |max| above 1.75 * 2^127 rounds to 2^128,
+ * which both types hold as infinity. */
+moe_status_t moe_mlp_dequantize_mxfp4(const uint8_t* q, const uint8_t* sf, int32_t groups, int64_t rows, int64_t cols,
+                                      int32_t dtype, void* dst, moe_stream_t stream);
+
+/* MXFP4 recipe forward (serving): moe_grouped_mlp_fwd with 4-bit weights and
+ * activations on the kind::mxf4 tensor cores (fp32 accumulation).  x is
+ * quantised along H, h = prob * silu(gate) * up (fp32) along I; out[t] =
+ * sum_j y[row(t, j)] (y kept in 24 bits as in moe_grouped_mlp_fwd, fp32 sum in
+ * ascending j, one bf16 rounding).  No backward: the recipe trains in MXFP8.
+ *   w1q, w1sf  MXFP4 tensor (2E, I, H): W_gate_up [E][2I][H], gate rows first.
+ *   w2q, w2sf  MXFP4 tensor (E, H, I): W_down.
+ *   routing    from moe_permute (xq may be NULL there).
+ *   x          bf16 [T][H];  out bf16 [T][H].
+ *   workspace  >= moe_workspace_size(MOE_OP_FWD_MXFP4, T, k, E, H, I), 256-byte
+ *              aligned.
+ * Limits as moe_grouped_mlp_fwd, and T*H < 2^34 - 2^27. */
+moe_status_t moe_grouped_mlp_fwd_mxfp4(const uint8_t* w1q, const uint8_t* w1sf, const uint8_t* w2q,
+                                       const uint8_t* w2sf, int32_t T, int32_t H, int32_t I, int32_t E, int32_t k,
+                                       int64_t rows_cap, const int32_t* split_sizes, const int32_t* group_offsets,
+                                       const int32_t* slot_to_row, const float* prob_perm, const void* x, void* out,
+                                       void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
 /* ----------------------------------------------------------- backward --- */
 

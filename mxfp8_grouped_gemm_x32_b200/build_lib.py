@@ -14,7 +14,8 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmoe_mxfp8.so")
 SOURCES = ["moe_mxfp8_all.cu", "api.cu", "gemm.cu", "permute.cu", "quant.cu", "swiglu_bwd.cu", "noalloc.cu", "router.cu",
            "scales.cu", "transpose.cu", "common.cuh", "gemm.cuh", "permute.cuh", "quant.cuh", "swiglu_bwd.cuh",
-           "router.cuh", "scales.cuh", "transpose.cuh"]
+           "router.cuh", "scales.cuh", "transpose.cuh", "router_loss.cu", "router_loss.cuh", "mxfp4.cu", "mxfp4.cuh",
+           "gemm_mxfp4.cu"]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared", "-diag-suppress", "550"]
 

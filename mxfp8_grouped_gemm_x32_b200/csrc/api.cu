@@ -7,11 +7,13 @@
 #include <vector>
 
 #include "gemm.cuh"
+#include "mxfp4.cuh"
 #include "permute.cuh"
 #include "quant.cuh"
 #include "swiglu_bwd.cuh"
 #include "transpose.cuh"
 #include "router.cuh"
+#include "router_loss.cuh"
 
 namespace moe {
 
@@ -58,6 +60,15 @@ namespace {
 inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool al32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 inline bool al256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+inline bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline bool al_elem(const void* p, int32_t dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == MOE_DTYPE_BF16 ? 1u : 3u)) == 0;
+}
+// 32-bit row and unit numbers in the MXFP4 quantisation kernels
+inline bool mxfp4_size_ok(int64_t groups, int64_t rows, int64_t cols) {
+  const int64_t lim = MXFP4_MAX_UNITS - (int64_t(1) << 24);  // and a grid's stride above
+  return rows < lim && cols / 8 < lim && rows * (cols / 8) < lim && groups * (rows * (cols / 8)) < lim;
+}
 inline int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
 inline moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
@@ -98,6 +109,21 @@ FwdBf16Ws carve_fwd_bf16(Carver& c, int64_t T, int64_t k, int64_t H, int64_t I, 
   w.xp = c.take(rows_cap * H * 2);  // gathered x, bf16, permuted order
   w.h = c.take(rows_cap * I * 2);   // h, bf16
   w.y = c.take(rows_cap * H * 4);   // fp32 down-projection rows in permuted order
+  return w;
+}
+
+// MXFP4 forward workspace: codes and scales of x (permuted rows) and of h, f24
+// rows.
+struct FwdMxfp4Ws {
+  uint8_t *xq, *xq_sf, *hq, *hq_sf, *y;
+};
+FwdMxfp4Ws carve_fwd_mxfp4(Carver& c, int64_t H, int64_t I, int64_t rows_cap) {
+  FwdMxfp4Ws w{};
+  w.xq = c.take(rows_cap * (H / 2));
+  w.xq_sf = c.take(mx_scale_bytes(1, rows_cap, H));
+  w.hq = c.take(rows_cap * (I / 2));
+  w.hq_sf = c.take(mx_scale_bytes(1, rows_cap, I));
+  w.y = c.take(rows_cap * H * 3);
   return w;
 }
 
@@ -310,6 +336,12 @@ int64_t moe_workspace_size(int32_t op, int32_t T, int32_t k, int32_t E, int32_t 
     case MOE_OP_BWD_FP8_TENSOR:
       if (H <= 0 || I <= 0) return -1;
       carve_bwd_f8t(c, T, k, H, I, E, rows_cap);
+      return c.off;
+    case MOE_OP_ROUTER_LOSSES:
+      return align256(router_loss_workspace_bytes(T, E));
+    case MOE_OP_FWD_MXFP4:
+      if (H <= 0 || I <= 0) return -1;
+      carve_fwd_mxfp4(c, H, I, rows_cap);
       return c.off;
   }
   return -1;
@@ -988,6 +1020,121 @@ moe_status_t moe_router_topk(const void* logits, int32_t logits_dtype, int32_t T
   TimeScope ts(st, "router");
   return cuda_status(launch_router_topk(logits, logits_dtype == MOE_DTYPE_BF16, T, E, k, topk_idx, topk_prob,
                                        nullptr, st));
+}
+
+moe_status_t moe_router_losses(const void* logits, int32_t logits_dtype, int32_t T, int32_t E, int32_t k,
+                               const uint8_t* token_mask, int32_t* topk_idx, float* topk_prob, float* lse,
+                               int32_t* counts, float* prob_sums, int32_t* tokens, float* losses, void* workspace,
+                               size_t workspace_bytes, moe_stream_t stream) {
+  if ((T > 0 && (!logits || !topk_idx || !topk_prob || !lse)) || T < 0) return MOE_ERR_INVALID;
+  if (!counts || !prob_sums || !tokens || !losses) return MOE_ERR_INVALID;
+  if (logits_dtype != MOE_DTYPE_F32 && logits_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID;
+  if (E <= 0 || k <= 0 || k > E) return MOE_ERR_INVALID;
+  if (!al_elem(logits, logits_dtype) || !al4(topk_idx) || !al4(topk_prob) || !al4(lse) || !al4(counts) ||
+      !al4(prob_sums) || !al4(tokens) || !al4(losses))
+    return MOE_ERR_INVALID;
+  if (E > MOE_MAX_EXPERTS || k > 32 || int64_t(T) * k >= (int64_t(1) << 30)) return MOE_ERR_UNSUPPORTED;
+  if (!workspace || !al16(workspace) ||
+      int64_t(workspace_bytes) < moe_workspace_size(MOE_OP_ROUTER_LOSSES, T, k, E, 0, 0))
+    return MOE_ERR_WORKSPACE;
+  if (!device_ok()) return MOE_ERR_NO_DEVICE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  TimeScope ts(st, "router_losses");
+  const RouterLossArgs a{logits, token_mask, T, E, k, topk_idx, topk_prob, lse, counts, prob_sums, tokens, losses};
+  return cuda_status(launch_router_losses(a, logits_dtype == MOE_DTYPE_BF16, workspace, st));
+}
+
+moe_status_t moe_router_bwd(const void* logits, int32_t logits_dtype, int32_t T, int32_t E, int32_t k,
+                            const uint8_t* token_mask, const int32_t* topk_idx, const float* topk_prob,
+                            const float* lse, const int32_t* counts, const int32_t* tokens, const float* dprob,
+                            const float* dlosses, void* dlogits, moe_stream_t stream) {
+  if (T < 0 || (T > 0 && (!logits || !topk_idx || !topk_prob || !lse || !dlogits))) return MOE_ERR_INVALID;
+  if (!counts || !tokens) return MOE_ERR_INVALID;
+  if (logits_dtype != MOE_DTYPE_F32 && logits_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID;
+  if (E <= 0 || k <= 0 || k > E) return MOE_ERR_INVALID;
+  if (!al_elem(logits, logits_dtype) || !al_elem(dlogits, logits_dtype) || !al4(topk_idx) || !al4(topk_prob) ||
+      !al4(lse) || !al4(counts) || !al4(tokens) || !al4(dprob) || !al4(dlosses))
+    return MOE_ERR_INVALID;
+  if (E > MOE_MAX_EXPERTS || k > 32 || int64_t(T) * k >= (int64_t(1) << 30)) return MOE_ERR_UNSUPPORTED;
+  if (!device_ok()) return MOE_ERR_NO_DEVICE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  TimeScope ts(st, "router_bwd");
+  const RouterBwdArgs a{logits, token_mask, T, E, k, topk_idx, topk_prob, lse, counts, tokens, dprob, dlosses,
+                        dlogits};
+  return cuda_status(launch_router_bwd(a, logits_dtype == MOE_DTYPE_BF16, st));
+}
+
+moe_status_t moe_mlp_quantize_mxfp4(const void* src, int32_t dtype, int32_t groups, int64_t rows, int64_t cols,
+                                    uint8_t* q, uint8_t* sf, moe_stream_t stream) {
+  if (groups < 0 || rows < 0 || cols < 0 || (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16))
+    return MOE_ERR_INVALID;
+  if (cols % 32) return MOE_ERR_UNSUPPORTED;
+  if (groups == 0 || rows == 0 || cols == 0) return MOE_OK;
+  if (!src || !q || !sf || !al16(src) || !al16(q) || !al16(sf)) return MOE_ERR_INVALID;
+  if (!mxfp4_size_ok(groups, rows, cols)) return MOE_ERR_UNSUPPORTED;
+  if (!device_ok()) return MOE_ERR_NO_DEVICE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  TimeScope ts(st, "quant_mxfp4");
+  return cuda_status(launch_mxfp4_quant(Mxfp4Args{src, nullptr, q, sf, groups, rows, cols}, dtype == MOE_DTYPE_BF16,
+                                        st));
+}
+
+moe_status_t moe_mlp_dequantize_mxfp4(const uint8_t* q, const uint8_t* sf, int32_t groups, int64_t rows, int64_t cols,
+                                      int32_t dtype, void* dst, moe_stream_t stream) {
+  if (groups < 0 || rows < 0 || cols < 0 || (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16))
+    return MOE_ERR_INVALID;
+  if (cols % 32) return MOE_ERR_UNSUPPORTED;
+  if (groups == 0 || rows == 0 || cols == 0) return MOE_OK;
+  if (!q || !sf || !dst || !al16(q) || !al16(sf) || !al16(dst)) return MOE_ERR_INVALID;
+  if (!mxfp4_size_ok(groups, rows, cols)) return MOE_ERR_UNSUPPORTED;
+  if (!device_ok()) return MOE_ERR_NO_DEVICE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  TimeScope ts(st, "dequant_mxfp4");
+  return cuda_status(launch_mxfp4_dequant(
+      Mxfp4Args{nullptr, dst, const_cast<uint8_t*>(q), const_cast<uint8_t*>(sf), groups, rows, cols},
+      dtype == MOE_DTYPE_BF16, st));
+}
+
+moe_status_t moe_grouped_mlp_fwd_mxfp4(const uint8_t* w1q, const uint8_t* w1sf, const uint8_t* w2q,
+                                       const uint8_t* w2sf, int32_t T, int32_t H, int32_t I, int32_t E, int32_t k,
+                                       int64_t rows_cap, const int32_t* split_sizes, const int32_t* group_offsets,
+                                       const int32_t* slot_to_row, const float* prob_perm, const void* x, void* out,
+                                       void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  if (!w1q || !w1sf || !w2q || !w2sf || !split_sizes || !group_offsets || !prob_perm ||
+      (T > 0 && (!x || !out || !slot_to_row)))
+    return MOE_ERR_INVALID;
+  if (!layer_dims_ok(T, H, I, E, k)) return MOE_ERR_UNSUPPORTED;
+  if (int64_t(T) * (H / 8) >= MXFP4_MAX_UNITS - (int64_t(1) << 24)) return MOE_ERR_UNSUPPORTED;
+  if (rows_cap < moe_padded_rows(T, k, E) || rows_cap % 128) return MOE_ERR_INVALID;
+  for (const void* p : {(const void*)w1q, (const void*)w1sf, (const void*)w2q, (const void*)w2sf, x,
+                        (const void*)out})
+    if (!al16(p)) return MOE_ERR_INVALID;
+  Carver c{static_cast<uint8_t*>(workspace)};
+  const FwdMxfp4Ws w = carve_fwd_mxfp4(c, H, I, rows_cap);
+  if (!workspace || !al256(workspace) || int64_t(workspace_bytes) < c.off) return MOE_ERR_WORKSPACE;
+  if (!device_ok()) return MOE_ERR_NO_DEVICE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) return MOE_OK;
+  {
+    TimeScope ts(st, "quant_x_mxfp4");
+    const Mxfp4ScatterArgs s{static_cast<const uint8_t*>(x), T, H, k, slot_to_row, w.xq, w.xq_sf};
+    if (launch_mxfp4_quant_scatter(s, st) != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  const int64_t R = int64_t(T) * k;
+  Gemm4Args g{};
+  g.E = E; g.group_offsets = group_offsets; g.split_sizes = split_sizes;
+  {
+    TimeScope ts(st, "gemm_gate_up_swiglu_mxfp4");
+    g.N = I; g.K = H; g.sfa = w.xq_sf; g.sfb = w1sf; g.prob = prob_perm; g.q_out = w.hq; g.sf_out = w.hq_sf;
+    if (launch_grouped_gemm_mxfp4(EPI4_SWIGLU, w.xq, rows_cap, w1q, g, R, st) != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  {
+    TimeScope ts(st, "gemm_down_mxfp4");
+    g.N = H; g.K = I; g.sfa = w.hq_sf; g.sfb = w2sf; g.out = w.y;
+    if (launch_grouped_gemm_mxfp4(EPI4_F24_ROWS, w.hq, rows_cap, w2q, g, R, st) != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  TimeScope ts(st, "combine");
+  return cuda_status(launch_combine(w.y, COMBINE_F24, slot_to_row, T, k, H, out, st));
 }
 
 moe_status_t moe_route_permute(const void* logits, int32_t logits_dtype, const void* x, int32_t T, int32_t H,

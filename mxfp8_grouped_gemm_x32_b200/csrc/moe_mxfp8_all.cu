@@ -8,4 +8,7 @@
 #include "transpose.cu"
 #include "noalloc.cu"
 #include "router.cu"
+#include "router_loss.cu"
 #include "scales.cu"
+#include "mxfp4.cu"
+#include "gemm_mxfp4.cu"

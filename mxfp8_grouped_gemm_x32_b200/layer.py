@@ -7,6 +7,10 @@ Steps (names of the C entry points):
                     for the forward and along the other axis for the backward
                     (forward only: moe_mlp_quantize_mxfp8 x2)
   route             moe_router_topk: router logits -> top-k experts + probabilities
+  route_losses      moe_router_losses: the same with the load-balance loss, the
+                    z-loss and the tokens per expert
+  route_backward    moe_router_bwd: gradient of the logits from d(prob) and the
+                    losses' gradients
   permute           moe_permute: counting sort by expert, gather + quantise x
   forward           moe_grouped_mlp_fwd: gate_up GEMM + ScaledSwiGLU + requant,
                     down GEMM, top-k combine
@@ -15,10 +19,15 @@ Steps (names of the C entry points):
   backward_bf16     moe_grouped_mlp_bwd_bf16: its backward
   forward_fp8_tensor / backward_fp8_tensor
                     moe_grouped_mlp_fwd/bwd_fp8_tensor: the per-tensor FP8 recipe
+  quantize_weights_mxfp4 / load_weights_mxfp4, forward_mxfp4
+                    moe_mlp_quantize_mxfp4, moe_grouped_mlp_fwd_mxfp4: the MXFP4
+                    (4-bit) serving recipe, routing from permute_index
   backward          moe_grouped_mlp_bwd: dgrad/wgrad of both projections,
                     ScaledSwiGLU backward, d(prob)
 """
 from __future__ import annotations
+
+import contextlib
 
 import torch
 
@@ -80,11 +89,31 @@ class _Alloc:
         return [name for name, t in self.tails if not bool((t == GUARD_BYTE).all())]
 
 
+_DTYPES = {torch.float32: lib.MOE_DTYPE_F32, torch.bfloat16: lib.MOE_DTYPE_BF16}
+
+
+def _logits_dtype(logits) -> int:
+    dt = _DTYPES.get(getattr(logits, "dtype", None))
+    if dt is None:
+        raise TypeError(f"logits: expected float32 or bfloat16, got {getattr(logits, 'dtype', type(logits).__name__)}")
+    return dt
+
+
+def on_device(dev: torch.device):
+    """Context in which `dev` is the current device (the library launches on
+    the current device; nothing to do when it already is)."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
 class GroupedMLP:
-    """One layer: T tokens, hidden H, intermediate I, E experts, top-k."""
+    """One layer: T tokens, hidden H, intermediate I, E experts, top-k.
+
+    mxfp8=False leaves out the buffers of the MXFP8 recipe (quantised weights,
+    x and h and its workspaces): a layer that routes and serves in MXFP4, or
+    runs one of the recipes on bf16 weights, does not need them."""
 
     def __init__(self, T: int, H: int, I: int, E: int, k: int, device="cuda", backward: bool = True,
-                 guard: int = 0):
+                 guard: int = 0, mxfp8: bool = True):
         self.T, self.H, self.I, self.E, self.k = T, H, I, E, k
         self.dev = torch.device(device)
         al = self._alloc = _Alloc(self.dev, guard)
@@ -92,11 +121,13 @@ class GroupedMLP:
         self.rows_cap = lib.moe_padded_rows(T, k, E)
         rc = self.rows_cap
         sb = lib.moe_mx_scale_bytes
-        # quantised weights (forward: along H for gate_up, along I for down)
-        self.w1q = u8(2 * E * I * H, "w1q")
-        self.w1sf = u8(sb(2 * E, I, H), "w1sf")
-        self.w2q = u8(E * H * I, "w2q")
-        self.w2sf = u8(sb(E, H, I), "w2sf")
+        self.mxfp8 = mxfp8
+        if mxfp8:
+            # quantised weights (forward: along H for gate_up, along I for down)
+            self.w1q = u8(2 * E * I * H, "w1q")
+            self.w1sf = u8(sb(2 * E, I, H), "w1sf")
+            self.w2q = u8(E * H * I, "w2q")
+            self.w2sf = u8(sb(E, H, I), "w2sf")
         # routing
         self.split_sizes = al.typed((E,), torch.int32, "split_sizes")
         self.group_offsets = al.typed((E + 1,), torch.int32, "group_offsets")
@@ -105,33 +136,42 @@ class GroupedMLP:
         self.topk_idx = al.typed((T, k), torch.int32, "topk_idx")        # router outputs
         self.topk_prob = al.typed((T, k), torch.float32, "topk_prob")
         self.prob_perm = al.typed((rc,), torch.float32, "prob_perm")
-        self.xq = u8(rc * H, "xq")
-        self.xq_sf = u8(sb(1, rc, H), "xq_sf")
-        self.hq = u8(rc * I, "hq")
-        self.hq_sf = u8(sb(1, rc, I), "hq_sf")
+        if mxfp8:
+            self.xq = u8(rc * H, "xq")
+            self.xq_sf = u8(sb(1, rc, H), "xq_sf")
+            self.hq = u8(rc * I, "hq")
+            self.hq_sf = u8(sb(1, rc, I), "hq_sf")
         self.out = al.typed((T, H), torch.bfloat16, "out")
         self.dev = self.out.device      # concrete device (index resolved) for the input checks
         self.ws_perm_bytes = lib.moe_workspace_size(lib.MOE_OP_PERMUTE, T, k, E, H, I)
-        self.ws_fwd_bytes = lib.moe_workspace_size(lib.MOE_OP_FWD, T, k, E, H, I)
         self.ws_perm = u8(self.ws_perm_bytes, "ws_perm")
-        self.ws_fwd = u8(self.ws_fwd_bytes, "ws_fwd")
+        if mxfp8:
+            self.ws_fwd_bytes = lib.moe_workspace_size(lib.MOE_OP_FWD, T, k, E, H, I)
+            self.ws_fwd = u8(self.ws_fwd_bytes, "ws_fwd")
         self.backward_enabled = backward
-        if backward:
+        if backward and mxfp8:
             self.w1tq = u8(E * H * 2 * I, "w1tq")
             self.w1tsf = u8(sb(E, H, 2 * I), "w1tsf")
             self.w2tq = u8(E * I * H, "w2tq")
             self.w2tsf = u8(sb(E, I, H), "w2tsf")
+            self.ws_bwd_bytes = lib.moe_workspace_size(lib.MOE_OP_BWD, T, k, E, H, I)
+            self.ws_bwd = u8(self.ws_bwd_bytes, "ws_bwd")
+        if backward:
             self.saved_a = al.typed((rc, 2 * I), torch.bfloat16, "saved_a")
             self.dX = al.typed((T, H), torch.bfloat16, "dX")
             self.dW1 = al.typed((E, 2 * I, H), torch.bfloat16, "dW1")
             self.dW2 = al.typed((E, H, I), torch.bfloat16, "dW2")
             self.dprob = al.typed((T, k), torch.float32, "dprob")
-            self.ws_bwd_bytes = lib.moe_workspace_size(lib.MOE_OP_BWD, T, k, E, H, I)
-            self.ws_bwd = u8(self.ws_bwd_bytes, "ws_bwd")
         else:
             self.saved_a = None
         self.xq_col = self.xq_col_sf = None   # x along tokens: only when permute(..., with_cols=True)
         self._x = None                         # the input of the last permutation (the backward's x)
+        self.router_lse = None                 # route_losses' outputs, once it has run
+        self.w1q4 = None                       # MXFP4 weights, once quantised or loaded
+
+    def _need_mxfp8(self):
+        if not self.mxfp8:
+            raise RuntimeError("this layer was built with mxfp8=False")
 
     def _cols(self, with_cols: bool):
         """Buffers of the optional column form of x (x^T quantised along
@@ -239,6 +279,121 @@ class GroupedMLP:
                                            self._stream())
         return self.dX, self.dW1, self.dW2, self.dprob
 
+    def route_losses(self, logits: torch.Tensor, token_mask: torch.Tensor = None):
+        """Router for training (moe_router_losses): logits fp32 or bf16
+        [T, E], token_mask bool [T] (False: padding) -> (topk_idx int32
+        [T, k], topk_prob fp32 [T, k], losses fp32 [2] = load-balance loss and
+        z-loss), in this layer's buffers; the tokens per expert land in
+        self.expert_counts (int32 [E]), the sums of the experts' softmax
+        probabilities in self.prob_sums (fp32 [E]), the number of unmasked
+        tokens in self.routed_tokens (int32 [1]).  For a loss over a
+        data-parallel job's whole batch, add the counts and tokens up over the
+        ranks before route_backward."""
+        T, E, k = self.T, self.E, self.k
+        dt = _logits_dtype(logits)
+        check_tensor(logits, "logits", logits.dtype, (T, E), self.dev)
+        if token_mask is not None:
+            check_tensor(token_mask, "token_mask", torch.bool, (T,), self.dev)
+        if self.router_lse is None:
+            al = self._alloc
+            self.router_lse = al.typed((T,), torch.float32, "router_lse")
+            self.expert_counts = al.typed((E,), torch.int32, "expert_counts")
+            self.prob_sums = al.typed((E,), torch.float32, "prob_sums")
+            self.routed_tokens = al.typed((1,), torch.int32, "routed_tokens")
+            self.router_losses = al.typed((2,), torch.float32, "router_losses")
+            self.ws_losses_bytes = lib.moe_workspace_size(lib.MOE_OP_ROUTER_LOSSES, T, k, E, 0, 0)
+            self.ws_losses = al.raw(self.ws_losses_bytes, "ws_losses")
+        with on_device(self.dev):
+            lib.moe_router_losses(logits.data_ptr(), dt, T, E, k, _ptr(token_mask), _ptr(self.topk_idx),
+                                  _ptr(self.topk_prob), _ptr(self.router_lse), _ptr(self.expert_counts),
+                                  _ptr(self.prob_sums), _ptr(self.routed_tokens), _ptr(self.router_losses),
+                                  _ptr(self.ws_losses), self.ws_losses_bytes, self._stream())
+        return self.topk_idx, self.topk_prob, self.router_losses
+
+    def route_backward(self, logits: torch.Tensor, dprob: torch.Tensor = None, dlosses: torch.Tensor = None,
+                       token_mask: torch.Tensor = None) -> torch.Tensor:
+        """Gradient of the logits (moe_router_bwd) after route_losses on the
+        same logits and mask: dprob fp32 [T, k] (as backward() returns it)
+        and dlosses fp32 [2], either None for zero -> dlogits [T, E] in the
+        logits' type, in a buffer of this layer."""
+        T, E, k = self.T, self.E, self.k
+        dt = _logits_dtype(logits)
+        check_tensor(logits, "logits", logits.dtype, (T, E), self.dev)
+        if self.router_lse is None:
+            raise RuntimeError("route_backward needs route_losses first")
+        if dprob is not None:
+            check_tensor(dprob, "dprob", torch.float32, (T, k), self.dev)
+        if dlosses is not None:
+            check_tensor(dlosses, "dlosses", torch.float32, (2,), self.dev)
+        if token_mask is not None:
+            check_tensor(token_mask, "token_mask", torch.bool, (T,), self.dev)
+        if getattr(self, "dlogits", None) is None or self.dlogits.dtype != logits.dtype:
+            self.dlogits = self._alloc.typed((T, E), logits.dtype, "dlogits")
+        with on_device(self.dev):
+            lib.moe_router_bwd(logits.data_ptr(), dt, T, E, k, _ptr(token_mask), _ptr(self.topk_idx),
+                               _ptr(self.topk_prob), _ptr(self.router_lse), _ptr(self.expert_counts),
+                               _ptr(self.routed_tokens), _ptr(dprob), _ptr(dlosses), _ptr(self.dlogits),
+                               self._stream())
+        return self.dlogits
+
+    def _mxfp4_weights(self):
+        if self.w1q4 is None:
+            u8, sb, E, H, I = self._alloc.raw, lib.moe_mx_scale_bytes, self.E, self.H, self.I
+            self.w1sf4 = u8(sb(2 * E, I, H), "w1sf4")
+            self.w2sf4 = u8(sb(E, H, I), "w2sf4")
+            self.w2q4 = u8(E * H * I // 2, "w2q4")
+            self.w1q4 = u8(E * I * H, "w1q4")
+
+    def quantize_weights_mxfp4(self, w1: torch.Tensor, w2: torch.Tensor) -> None:
+        """w1 bf16 [E, 2I, H] (gate rows first), w2 bf16 [E, H, I] -> this
+        layer's MXFP4 weights."""
+        E, H, I = self.E, self.H, self.I
+        check_tensor(w1, "w_gate_up", torch.bfloat16, (E, 2 * I, H), self.dev)
+        check_tensor(w2, "w_down", torch.bfloat16, (E, H, I), self.dev)
+        self._mxfp4_weights()
+        with on_device(self.dev):
+            s, bf = self._stream(), lib.MOE_DTYPE_BF16
+            lib.moe_mlp_quantize_mxfp4(w1.data_ptr(), bf, 2 * E, I, H, _ptr(self.w1q4), _ptr(self.w1sf4), s)
+            lib.moe_mlp_quantize_mxfp4(w2.data_ptr(), bf, E, H, I, _ptr(self.w2q4), _ptr(self.w2sf4), s)
+
+    def load_weights_mxfp4(self, w1_codes: torch.Tensor, w1_scales: torch.Tensor, w2_codes: torch.Tensor,
+                           w2_scales: torch.Tensor) -> None:
+        """Weights that are in 4 bits already (a checkpoint): uint8 codes
+        [E, 2I, H/2] (gate rows first) and [E, H, I/2], the even element in the
+        low half of a byte, and uint8 E8M0 scales in row order [E, 2I, H/32]
+        and [E, H, I/32].  Codes are copied, scales laid out for the GEMMs."""
+        E, H, I = self.E, self.H, self.I
+        check_tensor(w1_codes, "w1_codes", torch.uint8, (E, 2 * I, H // 2), self.dev)
+        check_tensor(w1_scales, "w1_scales", torch.uint8, (E, 2 * I, H // 32), self.dev)
+        check_tensor(w2_codes, "w2_codes", torch.uint8, (E, H, I // 2), self.dev)
+        check_tensor(w2_scales, "w2_scales", torch.uint8, (E, H, I // 32), self.dev)
+        self._mxfp4_weights()
+        with on_device(self.dev):
+            self.w1q4[: w1_codes.numel()].copy_(w1_codes.view(-1))
+            self.w2q4[: w2_codes.numel()].copy_(w2_codes.view(-1))
+            s = self._stream()
+            lib.moe_mx_scales_to_blocked(_ptr(w1_scales), 2 * E, I, H, H // 32, _ptr(self.w1sf4), s)
+            lib.moe_mx_scales_to_blocked(_ptr(w2_scales), E, H, I, I // 32, _ptr(self.w2sf4), s)
+
+    def forward_mxfp4(self, x: torch.Tensor) -> torch.Tensor:
+        """MXFP4 recipe forward (moe_grouped_mlp_fwd_mxfp4) on the routing of
+        the last permute / permute_index and the weights of the last
+        quantize_weights_mxfp4 / load_weights_mxfp4: x bf16 [T, H] -> out."""
+        E, H, I = self.E, self.H, self.I
+        if self.w1q4 is None:
+            raise RuntimeError("forward_mxfp4 needs quantize_weights_mxfp4 or load_weights_mxfp4 first")
+        check_tensor(x, "x", torch.bfloat16, (self.T, H), self.dev)
+        if getattr(self, "ws_mxfp4", None) is None:
+            self.ws_mxfp4_bytes = lib.moe_workspace_size(lib.MOE_OP_FWD_MXFP4, self.T, self.k, E, H, I)
+            self.ws_mxfp4 = self._alloc.raw(self.ws_mxfp4_bytes, "ws_mxfp4")
+        with on_device(self.dev):
+            lib.moe_grouped_mlp_fwd_mxfp4(_ptr(self.w1q4), _ptr(self.w1sf4), _ptr(self.w2q4), _ptr(self.w2sf4), self.T,
+                                          H, I, E, self.k, self.rows_cap, _ptr(self.split_sizes),
+                                          _ptr(self.group_offsets), _ptr(self.slot_to_row), _ptr(self.prob_perm),
+                                          x.data_ptr(), _ptr(self.out), _ptr(self.ws_mxfp4), self.ws_mxfp4_bytes,
+                                          self._stream())
+        return self.out
+
     def check_guards(self):
         """Names of the buffers written past their end (layers built with
         guard > 0; always empty otherwise)."""
@@ -250,6 +405,7 @@ class GroupedMLP:
 
     def quantize_weights(self, w1: torch.Tensor, w2: torch.Tensor) -> None:
         """w1 bf16 [E, 2I, H] (gate rows first), w2 bf16 [E, H, I]."""
+        self._need_mxfp8()
         E, H, I, s = self.E, self.H, self.I, self._stream()
         check_tensor(w1, "w_gate_up", torch.bfloat16, (E, 2 * I, H), self.dev)
         check_tensor(w2, "w_down", torch.bfloat16, (E, H, I), self.dev)
@@ -277,6 +433,7 @@ class GroupedMLP:
         """Router and permutation in one call (moe_route_permute): logits fp32
         or bf16 [T, E], x bf16 [T, H]; the routing lands in topk_idx /
         topk_prob, the quantised x in this layer's buffers."""
+        self._need_mxfp8()
         dt = {torch.float32: lib.MOE_DTYPE_F32, torch.bfloat16: lib.MOE_DTYPE_BF16}.get(logits.dtype)
         if dt is None:
             raise TypeError(f"logits: expected float32 or bfloat16, got {logits.dtype}")
@@ -296,6 +453,7 @@ class GroupedMLP:
         """x bf16 [T, H]; topk_idx int32 [T, k]; topk_prob float32 [T, k].
         with_cols also writes x^T quantised along tokens (xq_col), which the
         backward makes for itself from x."""
+        self._need_mxfp8()
         check_tensor(x, "x", torch.bfloat16, (self.T, self.H), self.dev)
         check_tensor(topk_idx, "topk_idx", torch.int32, (self.T, self.k), self.dev)
         check_tensor(topk_prob, "topk_prob", torch.float32, (self.T, self.k), self.dev)
@@ -308,6 +466,7 @@ class GroupedMLP:
         self._x = x
 
     def forward(self) -> torch.Tensor:
+        self._need_mxfp8()
         lib.moe_grouped_mlp_fwd(_ptr(self.w1q), _ptr(self.w1sf), _ptr(self.w2q), _ptr(self.w2sf), self.T,
                                 self.H, self.I, self.E, self.k, self.rows_cap, _ptr(self.split_sizes),
                                 _ptr(self.group_offsets), _ptr(self.row_to_slot), _ptr(self.slot_to_row),
@@ -319,6 +478,7 @@ class GroupedMLP:
 
     def backward(self, dY: torch.Tensor, x: torch.Tensor = None):
         """dY bf16 [T, H]; x defaults to the input of the last permutation."""
+        self._need_mxfp8()
         if not self.backward_enabled:
             raise RuntimeError("this layer was built with backward=False")
         x = self._x if x is None else x

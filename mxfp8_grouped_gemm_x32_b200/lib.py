@@ -24,6 +24,8 @@ MOE_OP_FWD_BF16 = 4
 MOE_OP_FWD_FP8_TENSOR = 5
 MOE_OP_BWD_BF16 = 6
 MOE_OP_BWD_FP8_TENSOR = 7
+MOE_OP_ROUTER_LOSSES = 8
+MOE_OP_FWD_MXFP4 = 9
 MOE_MAX_EXPERTS = 256
 
 STATUS = {
@@ -40,7 +42,8 @@ EXPORTED = [
     "moe_timing_enable", "moe_timing_read", "moe_permute_noalloc", "moe_mlp_quantize_weights",
     "moe_router_topk", "moe_mx_scales_to_blocked", "moe_mx_scales_from_blocked", "moe_route_permute",
     "moe_grouped_mlp_fwd_bf16", "moe_grouped_mlp_fwd_fp8_tensor", "moe_grouped_mlp_bwd_bf16",
-    "moe_grouped_mlp_bwd_fp8_tensor",
+    "moe_grouped_mlp_bwd_fp8_tensor", "moe_router_losses", "moe_router_bwd", "moe_mlp_quantize_mxfp4",
+    "moe_mlp_dequantize_mxfp4", "moe_grouped_mlp_fwd_mxfp4",
 ]
 MOE_DTYPE_F32, MOE_DTYPE_BF16 = 0, 1
 
@@ -94,6 +97,12 @@ _decl("moe_grouped_mlp_fwd_fp8_tensor", _I32, _P, _P, _I32, _I32, _I32, _I32, _I
       _P, _P, _P, _P, _SZ, _P)
 _decl("moe_grouped_mlp_bwd_fp8_tensor", _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I64, _P, _P, _P, _P, _P, _P,
       _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P)
+_decl("moe_router_losses", _I32, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P)
+_decl("moe_router_bwd", _I32, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P)
+_decl("moe_mlp_quantize_mxfp4", _I32, _P, _I32, _I32, _I64, _I64, _P, _P, _P)
+_decl("moe_mlp_dequantize_mxfp4", _I32, _P, _P, _I32, _I64, _I64, _I32, _P, _P)
+_decl("moe_grouped_mlp_fwd_mxfp4", _I32, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _I64, _P, _P, _P, _P, _P, _P,
+      _P, _SZ, _P)
 _decl("moe_get_device_status", _I32, _P)
 _decl("moe_status_string", ctypes.c_char_p, _I32)
 _decl("moe_launch_count", _I64, _I32)
@@ -222,6 +231,35 @@ def moe_grouped_mlp_bwd(w2tq, w2tsf, w1tq, w1tsf, T, H, I, E, k, rows_cap, split
         w2tq, w2tsf, w1tq, w1tsf, T, H, I, E, k, rows_cap, split_sizes, group_offsets, row_to_slot,
         slot_to_row, prob_perm, dY, saved_a, x, dX, dW1, dW2, dprob, workspace,
         workspace_bytes, stream))
+
+
+def moe_router_losses(logits, logits_dtype, T, E, k, token_mask, topk_idx, topk_prob, lse, counts, prob_sums, tokens,
+                      losses, workspace, workspace_bytes, stream=0):
+    _check("moe_router_losses", _lib.moe_router_losses(
+        logits, logits_dtype, T, E, k, token_mask, topk_idx, topk_prob, lse, counts, prob_sums, tokens, losses,
+        workspace, workspace_bytes, stream))
+
+
+def moe_router_bwd(logits, logits_dtype, T, E, k, token_mask, topk_idx, topk_prob, lse, counts, tokens, dprob,
+                   dlosses, dlogits, stream=0):
+    _check("moe_router_bwd", _lib.moe_router_bwd(
+        logits, logits_dtype, T, E, k, token_mask, topk_idx, topk_prob, lse, counts, tokens, dprob, dlosses, dlogits,
+        stream))
+
+
+def moe_mlp_quantize_mxfp4(src, dtype, groups, rows, cols, q, sf, stream=0):
+    _check("moe_mlp_quantize_mxfp4", _lib.moe_mlp_quantize_mxfp4(src, dtype, groups, rows, cols, q, sf, stream))
+
+
+def moe_mlp_dequantize_mxfp4(q, sf, groups, rows, cols, dtype, dst, stream=0):
+    _check("moe_mlp_dequantize_mxfp4", _lib.moe_mlp_dequantize_mxfp4(q, sf, groups, rows, cols, dtype, dst, stream))
+
+
+def moe_grouped_mlp_fwd_mxfp4(w1q, w1sf, w2q, w2sf, T, H, I, E, k, rows_cap, split_sizes, group_offsets, slot_to_row,
+                              prob_perm, x, out, workspace, workspace_bytes, stream=0):
+    _check("moe_grouped_mlp_fwd_mxfp4", _lib.moe_grouped_mlp_fwd_mxfp4(
+        w1q, w1sf, w2q, w2sf, T, H, I, E, k, rows_cap, split_sizes, group_offsets, slot_to_row, prob_perm, x, out,
+        workspace, workspace_bytes, stream))
 
 
 def moe_get_device_status(stream=0) -> int:

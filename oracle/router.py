@@ -42,3 +42,51 @@ def route_topk(logits: np.ndarray, k: int):
     with np.errstate(invalid="ignore"):
         top = top / top.sum(axis=1, keepdims=True)
     return order.astype(np.int32), top
+
+
+def route_losses(logits: np.ndarray, k: int, mask=None):
+    """The router's training outputs, from the definitions: ids and
+    probabilities of route_topk (probabilities 0 for masked tokens), tokens
+    per expert, sums of the softmax over all experts, the load-balance loss
+    E * sum_e (count_e / (n k)) * mean_t s_te and the z-loss
+    mean_t (log sum_e exp z_te)^2, over the n unmasked tokens (0 for none)."""
+    z = np.asarray(logits, np.float64)
+    T, E = z.shape
+    live = np.ones(T, bool) if mask is None else np.asarray(mask, bool)
+    idx, prob = route_topk(z, k)
+    prob = np.where(live[:, None], prob, 0.0)
+    n = int(live.sum())
+    counts = np.zeros(E, np.int64)
+    np.add.at(counts, idx[live].reshape(-1), 1)
+    zl = z[live]
+    with np.errstate(invalid="ignore"):
+        top = zl.max(axis=1, keepdims=True) if n else np.zeros((0, 1))
+        ex = np.exp(zl - top)
+        s = ex / ex.sum(axis=1, keepdims=True)
+        lse = (top + np.log(ex.sum(axis=1, keepdims=True)))[:, 0]
+    sums = s.sum(axis=0)
+    balance = E * float(np.sum(counts / (n * k) * (sums / n))) if n else 0.0
+    zloss = float(np.mean(lse ** 2)) if n else 0.0
+    full_s, full_l = np.zeros((T, E)), np.zeros(T)
+    full_s[live], full_l[live] = s, lse
+    return dict(idx=idx, prob=prob, counts=counts, sums=sums, n=n, losses=np.array([balance, zloss]), s=full_s,
+                lse=full_l, live=live, k=k)
+
+
+def route_backward(fwd: dict, dprob=None, dlosses=None):
+    """Gradient of the logits from those of the probabilities and the two
+    losses; the counts are constants."""
+    s, lse, live, k = fwd["s"], fwd["lse"], fwd["live"], fwd["k"]
+    T, E = s.shape
+    n = max(1, fwd["n"])
+    d = np.zeros((T, E))
+    if dlosses is not None:
+        f = fwd["counts"] / (n * k)
+        ds = np.broadcast_to(float(dlosses[0]) * E / n * f, (T, E))       # d balance / d s
+        d += s * (ds - np.sum(ds * s, axis=1, keepdims=True))             # softmax Jacobian
+        d += float(dlosses[1]) * 2.0 / n * lse[:, None] * s               # d lse / d z = s
+    if dprob is not None:
+        p, dp = fwd["prob"], np.asarray(dprob, np.float64)
+        inner = p * (dp - np.sum(p * dp, axis=1, keepdims=True))
+        np.add.at(d, (np.arange(T)[:, None], fwd["idx"]), inner)
+    return np.where(live[:, None], d, 0.0)
