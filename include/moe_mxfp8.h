@@ -420,9 +420,8 @@ moe_status_t moe_route_permute(const void* logits, int32_t logits_dtype, const v
  *   token_mask  NULL, or [T] bytes: 0 marks padding.  A masked token gets ids
  *               like any other (the layer's shapes stay) but probabilities 0
  *               and lse 0, and nothing of its logits counts, NaN included.
- *   topk_idx    int32 [T][k], as moe_router_topk;
- *   topk_prob   float [T][k], as moe_router_topk up to fp32 rounding (the
- *               sum over the kept experts runs in descending order here).
+ *   topk_idx    int32 [T][k], topk_prob float [T][k]: the bits that
+ *               moe_router_topk gives for the same logits.
  *   lse         float [T]; counts int32 [E]; prob_sums float [E]; tokens
  *               int32 [1] = n; losses float [2].
  *   workspace   >= moe_workspace_size(MOE_OP_ROUTER_LOSSES, T, k, E, 0, 0).

@@ -31,19 +31,29 @@ namespace {
 
 constexpr int RL_THREADS = 256;
 constexpr int RL_WARPS = RL_THREADS / 32;
-constexpr int RL_BLOCKS_PER_SM = 2;
+constexpr int RL_BLOCKS_PER_SM = 3;
 // most experts that a token of a group of G lanes keeps
 template <int G>
 constexpr int KEPT_MAX = G < 4 ? 8 * G : 32;
-constexpr int RF_CLUSTER = 8;  // blocks of the finishing cluster
+constexpr int RF_CLUSTER = 8, RF_THREADS = 1024;  // the finishing cluster
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+
+// 2^x by the hardware's instruction: relative error 2^-22, results below 2^-126
+// are 0.  As exp(x) = 2^(x log2(e)) the product's rounding adds 2^-24 |x|
+// log2(e) -- for softmax terms, which are small where |x| is large.
+constexpr float LOG2E = 1.4426950408889634f;
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // Experts 8g..8g+7 of row t; experts past E read as -inf.  `vec`: rows start
 // on 16-byte boundaries and E is a multiple of 8.
 template <bool BF16>
-__device__ __forceinline__ void load_row8(const void* p, int64_t t, int E, int g, bool vec, float* v) {
-  const int64_t base = t * E + 8 * g;
+__device__ __forceinline__ void load_row8(const void* p, int t, int E, int g, bool vec, float* v) {
+  const int64_t base = int64_t(t) * E + 8 * g;
   if (8 * g >= E) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = neg_inf();
@@ -73,8 +83,8 @@ __device__ __forceinline__ void load_row8(const void* p, int64_t t, int E, int g
 }
 
 template <bool BF16>
-__device__ __forceinline__ void store_row8(void* p, int64_t t, int E, int g, bool vec, const float* v) {
-  const int64_t base = t * E + 8 * g;
+__device__ __forceinline__ void store_row8(void* p, int t, int E, int g, bool vec, const float* v) {
+  const int64_t base = int64_t(t) * E + 8 * g;
   if (8 * g >= E) return;
   if constexpr (BF16) {
     uint16_t* q = static_cast<uint16_t*>(p) + base;
@@ -99,12 +109,86 @@ __device__ __forceinline__ void store_row8(void* p, int64_t t, int E, int g, boo
   }
 }
 
-// Sum over the G lanes of a group, the same in each of them.
+// Sum and maximum over the G lanes of a group, the same in each of them.
 template <int G>
 __device__ __forceinline__ float group_sum(float x) {
 #pragma unroll
   for (int off = G / 2; off >= 1; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
   return x;
+}
+template <int G>
+__device__ __forceinline__ float group_max(float x) {
+  if constexpr (G == 32) {
+    float m;  // one instruction for the whole warp (sm_100a)
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+    return m;
+  } else {
+#pragma unroll
+    for (int off = G / 2; off >= 1; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, off));
+    return x;
+  }
+}
+
+// A lane's two best candidates among its experts, best first: value and tag, the
+// tag one bit (0..7) for the number among the lane's eight with the lane's place
+// in the group above it.  Equal values: the lower number first.  NaN stands
+// where there is no candidate: it wins no maximum and equals nothing.
+struct Best {
+  float m1, m2;
+  uint32_t t1, t2;
+};
+__device__ __forceinline__ int tag_expert(uint32_t tag) { return 8 * int(tag >> 8) + __ffs(int(tag & 0xFFu)) - 1; }
+
+// The two best of eight values, by merging sorted pairs (50 instructions; one
+// value at a time takes 64).
+__device__ __forceinline__ Best best_of8(const float* v, uint32_t place) {
+  float a1[4], a2[4];
+  uint32_t x1[4], x2[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const bool p = v[2 * j + 1] > v[2 * j];
+    a1[j] = p ? v[2 * j + 1] : v[2 * j];
+    a2[j] = p ? v[2 * j] : v[2 * j + 1];
+    x1[j] = p ? 2u << (2 * j) : 1u << (2 * j);
+    x2[j] = p ? 1u << (2 * j) : 2u << (2 * j);
+  }
+#pragma unroll
+  for (int w = 2; w >= 1; w /= 2)
+#pragma unroll
+    for (int j = 0; j < w; ++j) {
+      // lists 2j and 2j + 1: the numbers of the first are below the second's
+      const bool p = a1[2 * j + 1] > a1[2 * j];
+      const float lose = p ? a1[2 * j] : a1[2 * j + 1], next = p ? a2[2 * j + 1] : a2[2 * j];
+      const uint32_t lx = p ? x1[2 * j] : x1[2 * j + 1], nx = p ? x2[2 * j + 1] : x2[2 * j];
+      const bool q = next > lose || (!p && next == lose);
+      const float top = p ? a1[2 * j + 1] : a1[2 * j];
+      const uint32_t tx = p ? x1[2 * j + 1] : x1[2 * j];
+      a1[j] = top;
+      x1[j] = tx;
+      a2[j] = q ? next : lose;
+      x2[j] = q ? nx : lx;
+    }
+  return Best{a1[0], a2[0], x1[0] | place, x2[0] | place};
+}
+
+// The two best of the values whose bit in `used` is not set (none of them NaN).
+__device__ __forceinline__ Best best_unused(const float* v, uint32_t used, uint32_t place) {
+  const float none = __int_as_float(0x7FC00000);
+  Best b{none, none, place, place};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if ((used >> i) & 1u) continue;
+    if (!(v[i] <= b.m1)) {  // larger, or the first
+      b.m2 = b.m1;
+      b.t2 = b.t1;
+      b.m1 = v[i];
+      b.t1 = place | (1u << i);
+    } else if (!(v[i] <= b.m2)) {
+      b.m2 = v[i];
+      b.t2 = place | (1u << i);
+    }
+  }
+  return b;
 }
 
 struct LossPartials {
@@ -114,105 +198,152 @@ struct LossPartials {
   int32_t* n;       // [blocks]
 };
 
+// Selection: k rounds of a maximum over the group's lanes, each of which offers
+// the best of its experts not yet kept.  A lane prepares its two best at once
+// and looks again only after both were kept, which for 256 experts and k = 8
+// happens about once per token -- a round is then a handful of instructions
+// instead of a scan of eight values.  The lane that wins writes the kept value
+// and id to shared memory; equal values go to the lowest lane, whose experts
+// have the lower ids.
 template <bool BF16, int G>
-__global__ void __launch_bounds__(RL_THREADS) router_loss_kernel(const RouterLossArgs a, const LossPartials part,
-                                                                 const bool vec) {
+__global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM)
+    router_loss_kernel(const RouterLossArgs a, const LossPartials part, const bool vec) {
   constexpr int GROUPS = 32 / G;               // tokens per warp
-  __shared__ float list[RL_WARPS * GROUPS][KEPT_MAX<G> + 1];  // unnormalised probabilities of a token's kept experts
-  __shared__ int32_t ids[RL_WARPS * GROUPS][KEPT_MAX<G> + 1];
+  constexpr int KL = (KEPT_MAX<G> + G - 1) / G;  // kept experts per lane
+  __shared__ float2 list[RL_WARPS * GROUPS][KEPT_MAX<G> + 1];  // (value, id as bits) of a token's kept experts
   __shared__ float bsum[RL_WARPS][8 * G];
   __shared__ int32_t bcnt[RL_WARPS][8 * G];
   __shared__ float bz[RL_WARPS];
   __shared__ int32_t bn[RL_WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane & (G - 1), sub = lane / G;
+  const uint32_t upto_me = (0xFFFFFFFFu >> (31 - lane)) & ~((1u << (sub * G)) - 1u);  // this group's lanes up to this one
   const int slot = warp * GROUPS + sub;
   const int E = a.E, k = a.k;
+  const uint32_t place = uint32_t(g) << 8;
+  // bits of the numbers that are no expert
+  const uint32_t none = 8 * g >= E ? 0xFFu : (8 * g + 8 <= E ? 0u : (0xFFu << (E - 8 * g)) & 0xFFu);
   float acc[8], zsum = 0.0f;
   int32_t cnt[8], n = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.0f, cnt[i] = 0;
-  const int64_t per = int64_t(RL_WARPS) * GROUPS;
+  // counts of up to 255 tokens in bytes, then added to the words above
+  uint32_t cnt_lo = 0, cnt_hi = 0, tokens = 0;
+  auto spill_counts = [&] {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      cnt[i] += int32_t((cnt_lo >> (8 * i)) & 0xFFu);
+      cnt[4 + i] += int32_t((cnt_hi >> (8 * i)) & 0xFFu);
+    }
+    cnt_lo = cnt_hi = tokens = 0;
+  };
+  constexpr int per = RL_WARPS * GROUPS;  // tokens per block and pass (T < 2^30: 32-bit token numbers)
   // whole warps take part in every round of shuffles: a group past the last
   // token works on the last one and keeps nothing
-  for (int64_t t0 = int64_t(blockIdx.x) * per + warp * GROUPS; t0 < a.T; t0 += int64_t(gridDim.x) * per) {
+  const int step = int(gridDim.x) * per;
+  int t0 = int(blockIdx.x) * per + warp * GROUPS;
+  float next[8];  // the logits of the token after this one are on their way
+  if (t0 < a.T) load_row8<BF16>(a.logits, min(t0 + sub, a.T - 1), E, g, vec, next);
+  for (; t0 < a.T; t0 += step) {
     const bool in = t0 + sub < a.T;
-    const int64_t t = in ? t0 + sub : int64_t(a.T) - 1;
+    const int t = in ? t0 + sub : a.T - 1;
     const bool live = in && (!a.mask || a.mask[t] != 0);
     float v[8];
-    load_row8<BF16>(a.logits, t, E, g, vec, v);
-    bool nan = false;
-    uint32_t used = 0;  // bit i: expert 8g + i is kept or does not exist
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (v[i] != v[i]) {
-        nan = true;
-        v[i] = neg_inf();  // NaN ranks last
-      }
-      if (8 * g + i >= E) used |= 1u << i;
-    }
-    const uint32_t none = used;
-    float m = 0.0f, total = 0.0f;
-    for (int r = 0; r < k; ++r) {
-      float bv = neg_inf();
-      int be = 0x7fffffff;
+    for (int i = 0; i < 8; ++i) v[i] = next[i];
+    if (t0 + step < a.T) load_row8<BF16>(a.logits, min(t0 + step + sub, a.T - 1), E, g, vec, next);
+    // a NaN among the lane's logits makes this sum NaN (and so may infinities)
+    bool nan = false;
+    const float probe = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    if (probe != probe) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (!((used >> i) & 1u) && (v[i] > bv || be == 0x7fffffff)) {
-          bv = v[i];
-          be = 8 * g + i;
+        if (v[i] != v[i]) {
+          nan = true;
+          v[i] = neg_inf();  // NaN ranks last
         }
-#pragma unroll
-      for (int off = G / 2; off >= 1; off >>= 1) {
-        const float ov = __shfl_xor_sync(0xFFFFFFFFu, bv, off);
-        const int oe = __shfl_xor_sync(0xFFFFFFFFu, be, off);
-        if (ov > bv || (ov == bv && oe < be)) {
-          bv = ov;
-          be = oe;
-        }
+    }
+    uint32_t used = none;
+    Best b = none ? best_unused(v, used, place) : best_of8(v, place);
+    float top = group_max<G>(b.m1);
+    const float m = top;
+    float2* slot_list = list[slot];
+    for (int r = 0; r < k; ++r) {
+      // the lowest of the group's lanes that hold the maximum
+      if ((__ballot_sync(0xFFFFFFFFu, b.m1 == top) & upto_me) == (1u << lane)) {
+        slot_list[r] = make_float2(b.m1, __uint_as_float(b.t1));
+        used |= b.t1;
+        b.m1 = b.m2;
+        b.t1 = b.t2;
+        b.m2 = __int_as_float(0x7FC00000);
+        if (b.m1 != b.m1) b = best_unused(v, used, place);
       }
-      if ((be >> 3) == g) used |= 1u << (be & 7);
-      if (r == 0) m = bv;
-      const float ex = expf(bv - m);
-      total += ex;
-      if (g == 0) {
-        list[slot][r] = ex;
-        ids[slot][r] = be;
-      }
+      top = group_max<G>(b.m1);
     }
     __syncwarp();
-    if (in)
-      for (int r = g; r < k; r += G) {
-        a.topk_idx[t * k + r] = ids[slot][r];
-        a.topk_prob[t * k + r] = live ? list[slot][r] / total : 0.0f;
+    // probabilities of the kept experts; the sum runs over 32 places as a
+    // butterfly, kept expert r in place r -- the order of moe_router_topk
+    float ex[KL];
+    int32_t id[KL];
+#pragma unroll
+    for (int j = 0; j < KL; ++j) {
+      const int r = g + j * G;
+      ex[j] = 0.0f;
+      if (r < k) {
+        const float2 x = list[slot][r];
+        ex[j] = expf(x.x - m);
+        id[j] = tag_expert(__float_as_uint(x.y));
       }
-    __syncwarp();
-    // softmax over all experts
-    float e[8], se = 0.0f;
+    }
+    float tree[KL];
+#pragma unroll
+    for (int j = 0; j < KL; ++j) tree[j] = ex[j];
+#pragma unroll
+    for (int w = KL / 2; w >= 1; w /= 2)
+#pragma unroll
+      for (int j = 0; j < w; ++j) tree[j] += tree[j + w];
+    const float total = group_sum<G>(tree[0]);
+    if (in) {
+#pragma unroll
+      for (int j = 0; j < KL; ++j) {
+        const int r = g + j * G;
+        if (r < k) {
+          a.topk_idx[int64_t(t) * k + r] = id[j];
+          a.topk_prob[int64_t(t) * k + r] = live ? ex[j] / total : 0.0f;
+        }
+      }
+    }
+    __syncwarp();  // the list is read before the next token's is written
+    // softmax over all experts (what is no expert holds -inf and adds 0).  The
+    // product m log2(e) is rounded once for all terms: a factor 1 +- 2^-24 |m|
+    // that cancels in s and moves lse by less than its own rounding
+    float se = 0.0f;
+    const float ml = m * LOG2E;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      e[i] = expf(v[i] - m);
-      if ((none >> i) & 1u) e[i] = 0.0f;
-      se += e[i];
+      v[i] = fast_exp2(fmaf(v[i], LOG2E, -ml));
+      se += v[i];
     }
     if (nan) se = __int_as_float(0x7FC00000);
     se = group_sum<G>(se);
-    const float lse = live ? m + logf(se) : 0.0f;
+    const float lse = live ? m + __logf(se) : 0.0f;  // se >= 1: 2^-21 absolute
     if (in && g == 0) a.lse[t] = lse;
     if (live) {
-      const float inv = 1.0f / se;
-      used &= ~none;
+      const float inv = __fdividef(1.0f, se);
+      const uint32_t kept = used & ~none & 0xFFu;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        acc[i] += e[i] * inv;
-        cnt[i] += int32_t((used >> i) & 1u);
-      }
+      for (int i = 0; i < 8; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
+      // bits 0..3 and 4..7 of `kept` to the bytes of two words
+      cnt_lo += ((kept & 15u) * 0x00204081u) & 0x01010101u;
+      cnt_hi += ((kept >> 4) * 0x00204081u) & 0x01010101u;
       if (g == 0) {
         zsum += lse * lse;
         n += 1;
       }
     }
+    if (++tokens == 255) spill_counts();
   }
+  spill_counts();
   // the block's sums: over the warp's groups by shuffles, over the warps in order
 #pragma unroll
   for (int off = G; off < 32; off <<= 1) {
@@ -259,62 +390,78 @@ __global__ void __launch_bounds__(RL_THREADS) router_loss_kernel(const RouterLos
   }
 }
 
-// Sum over the block in a fixed order, the same in every thread.
+// Sum over the finishing block in a fixed order, the same in every thread.
 __device__ __forceinline__ double block_sum(double x, double* buf) {
   __syncthreads();
   buf[threadIdx.x] = x;
   __syncthreads();
-  for (int s = RL_THREADS / 2; s >= 1; s >>= 1) {
+  for (int s = RF_THREADS / 2; s >= 1; s >>= 1) {
     if (int(threadIdx.x) < s) buf[threadIdx.x] += buf[threadIdx.x + s];
     __syncthreads();
   }
   return buf[0];
 }
 
-// One cluster adds the blocks' rows up: block c owns the experts c, c + 8, ...
-// in runs of 32 (lanes) x 8 slices of the rows (warps).  Sums in 64 bits: a
-// few hundred terms of any size, and no cost next to the loads.
-__global__ void __cluster_dims__(RF_CLUSTER, 1, 1) __launch_bounds__(RL_THREADS)
+// One cluster adds the blocks' rows up: block c owns the experts 32 c .. 32 c +
+// 31, one per lane, its warps every 32nd row, four loads in flight each.
+// Sums in 64 bits: a few hundred terms of any size, and no cost next to the
+// loads.
+__global__ void __cluster_dims__(RF_CLUSTER, 1, 1) __launch_bounds__(RF_THREADS)
     router_loss_finish_kernel(const RouterLossArgs a, const LossPartials part, const int blocks) {
-  __shared__ double buf[RL_THREADS];
-  __shared__ int32_t ibuf[RL_WARPS][32];
+  __shared__ double buf[RF_THREADS];
+  __shared__ int32_t ibuf[RF_THREADS / 32][32];
   __shared__ double mine;  // this block's part of sum_e counts_e sums_e
+  static_assert(32 * RF_CLUSTER >= MOE_MAX_EXPERTS, "an expert per lane of the cluster");
+  constexpr int W = RF_THREADS / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = int(cluster_ctarank());
-  double dot = 0.0;
-  for (int e0 = 32 * c; e0 < a.E; e0 += 32 * RF_CLUSTER) {
-    const int e = e0 + lane;
-    double s = 0.0;
-    int32_t n = 0;
-    if (e < a.E)
-      for (int b = warp; b < blocks; b += RL_WARPS) {
-        s += double(part.sums[int64_t(b) * a.E + e]);
-        n += part.counts[int64_t(b) * a.E + e];
+  const int e = 32 * c + lane;
+  double s = 0.0;
+  int32_t cnt = 0;
+  if (e < a.E)
+    for (int b0 = warp; b0 < blocks; b0 += 4 * W) {
+      float x[4];
+      int32_t y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int b = b0 + i * W;
+        x[i] = b < blocks ? part.sums[int64_t(b) * a.E + e] : 0.0f;
+        y[i] = b < blocks ? part.counts[int64_t(b) * a.E + e] : 0;
       }
-    __syncthreads();
-    buf[threadIdx.x] = s;
-    ibuf[warp][lane] = n;
-    __syncthreads();
-    if (warp == 0 && e < a.E) {
-      s = 0.0;
-      n = 0;
-      for (int w = 0; w < RL_WARPS; ++w) {
-        s += buf[32 * w + lane];
-        n += ibuf[w][lane];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s += double(x[i]);
+        cnt += y[i];
       }
-      a.prob_sums[e] = float(s);
-      a.counts[e] = n;
-      dot += s * double(n);
     }
-  }
-  const double all = block_sum(dot, buf);
-  if (threadIdx.x == 0) mine = all;
   double z = 0.0, n = 0.0;
-  if (c == 0) {
-    for (int b = threadIdx.x; b < blocks; b += RL_THREADS) {
+  if (c == 0)
+    for (int b = threadIdx.x; b < blocks; b += RF_THREADS) {
       z += double(part.z[b]);
       n += double(part.n[b]);  // exact: below 2^53
     }
+  buf[threadIdx.x] = s;
+  ibuf[warp][lane] = cnt;
+  __syncthreads();
+  if (warp == 0) {
+    double dot = 0.0;
+    if (e < a.E) {
+      s = 0.0;
+      cnt = 0;
+#pragma unroll 8
+      for (int w = 0; w < W; ++w) {
+        s += buf[32 * w + lane];
+        cnt += ibuf[w][lane];
+      }
+      a.prob_sums[e] = float(s);
+      a.counts[e] = cnt;
+      dot = s * double(cnt);
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, off);
+    if (lane == 0) mine = dot;
+  }
+  if (c == 0) {
     z = block_sum(z, buf);
     n = block_sum(n, buf);
   }
@@ -333,14 +480,16 @@ __global__ void __cluster_dims__(RF_CLUSTER, 1, 1) __launch_bounds__(RL_THREADS)
   cluster_sync_all();  // no block leaves while its shared memory is read
 }
 
-// Gradient of the logits.  A lane's eight gradients go through its own words of
-// shared memory so that the token's kept experts can be added by index, in
-// ascending order (an expert that a token lists twice gets both).
+// Gradient of the logits, on the same lanes.  The k kept logits' gradients are
+// scattered to a zeroed row of shared memory, from which every lane adds its
+// eight; only where a token lists an expert twice are they added one by one.
 template <bool BF16, int G>
-__global__ void __launch_bounds__(RL_THREADS) router_bwd_kernel(const RouterBwdArgs a, const bool vec) {
+__global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM) router_bwd_kernel(const RouterBwdArgs a, const bool vec) {
   constexpr int GROUPS = 32 / G;
+  constexpr int KL = (KEPT_MAX<G> + G - 1) / G;  // kept experts per lane
   __shared__ float share[8 * G];                      // f_e
-  __shared__ __align__(16) float grad[RL_THREADS][8];
+  __shared__ __align__(16) float add[RL_WARPS * GROUPS][8 * G];  // gradients of a token's kept logits, else 0
+  __shared__ uint8_t who[RL_WARPS * GROUPS][8 * G];
   __shared__ float2 list[RL_WARPS * GROUPS][KEPT_MAX<G> + 1];  // (id as bits, gradient of the kept logit)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane & (G - 1), sub = lane / G;
@@ -348,24 +497,59 @@ __global__ void __launch_bounds__(RL_THREADS) router_bwd_kernel(const RouterBwdA
   const int E = a.E, k = a.k;
   const float n = float(max(*a.tokens, 1));
   for (int e = threadIdx.x; e < 8 * G; e += RL_THREADS) share[e] = e < E ? float(a.counts[e]) / (n * float(k)) : 0.0f;
+  for (int i = threadIdx.x; i < RL_WARPS * GROUPS * 8 * G; i += RL_THREADS) (&add[0][0])[i] = 0.0f;
   __syncthreads();
   const float cb = a.dlosses ? a.dlosses[0] * float(E) / n : 0.0f;
   const float cz = a.dlosses ? a.dlosses[1] * 2.0f / n : 0.0f;
   float f[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = share[8 * g + i];
-  const int64_t per = int64_t(RL_WARPS) * GROUPS;
-  for (int64_t t0 = int64_t(blockIdx.x) * per + warp * GROUPS; t0 < a.T; t0 += int64_t(gridDim.x) * per) {
-    const bool in = t0 + sub < a.T;
-    const int64_t t = in ? t0 + sub : int64_t(a.T) - 1;
-    const bool live = in && (!a.mask || a.mask[t] != 0);
-    float d[8];
-    const float lse = a.lse[t];
-    load_row8<BF16>(a.logits, t, E, g, vec, d);
+  constexpr int per = RL_WARPS * GROUPS;  // tokens per block and pass (T < 2^30: 32-bit token numbers)
+  // a token's inputs are loaded while the one before it is worked on
+  float next[8], next_lse, p_next[KL], dp_next[KL];
+  int32_t id_next[KL];
+  bool live_next;
+  auto fetch = [&](int t0) {
+    const int t = min(t0 + sub, a.T - 1);
+    load_row8<BF16>(a.logits, t, E, g, vec, next);
+    next_lse = a.lse[t];
+    live_next = t0 + sub < a.T && (!a.mask || a.mask[t] != 0);
+    if (a.dprob) {
+#pragma unroll
+      for (int j = 0; j < KL; ++j) {
+        const int r = g + j * G;
+        p_next[j] = dp_next[j] = 0.0f;
+        id_next[j] = 0;
+        if (r < k) {
+          p_next[j] = a.topk_prob[int64_t(t) * k + r];
+          dp_next[j] = a.dprob[int64_t(t) * k + r];
+          id_next[j] = a.topk_idx[int64_t(t) * k + r];
+        }
+      }
+    }
+  };
+  const int step = int(gridDim.x) * per;
+  int t0 = int(blockIdx.x) * per + warp * GROUPS;
+  if (t0 < a.T) fetch(t0);
+  for (; t0 < a.T; t0 += step) {
+    const int t = t0 + sub;
+    const bool in = t < a.T, live = live_next;
+    const float lse = next_lse;
+    float d[8], p[KL], dp[KL];
+    int32_t id[KL];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[i] = next[i];
+#pragma unroll
+    for (int j = 0; j < KL; ++j) {
+      p[j] = p_next[j];
+      dp[j] = dp_next[j];
+      id[j] = id_next[j];
+    }
+    if (t0 + step < a.T) fetch(t0 + step);
     float fs = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      d[i] = 8 * g + i < E ? expf(d[i] - lse) : 0.0f;  // s
+      d[i] = fast_exp2((d[i] - lse) * LOG2E);  // s (0 where there is no expert)
       fs = fmaf(d[i], f[i], fs);
     }
     fs = group_sum<G>(fs);
@@ -373,26 +557,50 @@ __global__ void __launch_bounds__(RL_THREADS) router_bwd_kernel(const RouterBwdA
     for (int i = 0; i < 8; ++i) d[i] *= fmaf(cb, f[i] - fs, cz * lse);
     if (a.dprob) {
       float dot = 0.0f;
-      for (int r = g; r < k; r += G) dot = fmaf(a.topk_prob[t * k + r], a.dprob[t * k + r], dot);
+#pragma unroll
+      for (int j = 0; j < KL; ++j) dot = fmaf(p[j], dp[j], dot);
       dot = group_sum<G>(dot);
-      __syncwarp();
-      for (int r = g; r < k; r += G) {
-        const int32_t e = a.topk_idx[t * k + r];
-        if (in && (e < 0 || e >= E)) set_status(MOE_ERR_DEVICE_INDEX);
-        list[slot][r] = make_float2(__int_as_float(e), a.topk_prob[t * k + r] * (a.dprob[t * k + r] - dot));
+#pragma unroll
+      for (int j = 0; j < KL; ++j) {
+        const int r = g + j * G;
+        if (r < k) {
+          if (in && uint32_t(id[j]) >= uint32_t(E)) set_status(MOE_ERR_DEVICE_INDEX);
+          list[slot][r] = make_float2(__int_as_float(id[j]), p[j] * (dp[j] - dot));
+        }
       }
-      float4* own = reinterpret_cast<float4*>(grad[threadIdx.x]);
-      own[0] = make_float4(d[0], d[1], d[2], d[3]);
-      own[1] = make_float4(d[4], d[5], d[6], d[7]);
+      float* own = add[slot];
       __syncwarp();
-      for (int r = 0; r < k; ++r) {
-        const float2 x = list[slot][r];
-        const int64_t i = int64_t(__float_as_int(x.x)) - 8 * g;  // ids outside [0, E) belong to no lane's experts
-        if (i >= 0 && i < 8 && 8 * g + i < E) grad[threadIdx.x][i] += x.y;
+      // each kept expert's gradient to its place, and the number r beside it: a
+      // number that is read back as another one tells of an id listed twice
+#pragma unroll
+      for (int j = 0; j < KL; ++j)
+        if (g + j * G < k && uint32_t(id[j]) < uint32_t(E)) {
+          own[id[j]] = list[slot][g + j * G].y;
+          who[slot][id[j]] = uint8_t(g + j * G);
+        }
+      __syncwarp();
+      bool twice = false;
+#pragma unroll
+      for (int j = 0; j < KL; ++j)
+        if (g + j * G < k && uint32_t(id[j]) < uint32_t(E)) twice |= who[slot][id[j]] != uint8_t(g + j * G);
+      if (__any_sync(0xFFFFFFFFu, twice)) {
+        // in ascending order of r, by the lane that owns the expert
+        for (int r = 0; r < k; ++r) {
+          const float2 x = list[slot][r];
+          const uint32_t i = uint32_t(__float_as_int(x.x)) - 8u * uint32_t(g);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (i == uint32_t(e)) d[e] += x.y;
+        }
+      } else {
+        const float4 lo = reinterpret_cast<const float4*>(own)[2 * g], hi = reinterpret_cast<const float4*>(own)[2 * g + 1];
+        d[0] += lo.x; d[1] += lo.y; d[2] += lo.z; d[3] += lo.w;
+        d[4] += hi.x; d[5] += hi.y; d[6] += hi.z; d[7] += hi.w;
       }
-      const float4 lo = own[0], hi = own[1];
-      d[0] = lo.x; d[1] = lo.y; d[2] = lo.z; d[3] = lo.w;
-      d[4] = hi.x; d[5] = hi.y; d[6] = hi.z; d[7] = hi.w;
+      __syncwarp();  // read before the next token's values are written; the places go back to 0
+#pragma unroll
+      for (int j = 0; j < KL; ++j)
+        if (g + j * G < k && uint32_t(id[j]) < uint32_t(E)) own[id[j]] = 0.0f;
     }
     if (!live) {
 #pragma unroll
@@ -458,14 +666,14 @@ cudaError_t launch_router_losses(const RouterLossArgs& a, bool bf16, void* ws, c
     if (e != cudaSuccess) return e;
     count_launch();
   }
-  router_loss_finish_kernel<<<RF_CLUSTER, RL_THREADS, 0, st>>>(a, part, int(blocks));
+  router_loss_finish_kernel<<<RF_CLUSTER, RF_THREADS, 0, st>>>(a, part, int(blocks));
   count_launch();
   return cudaGetLastError();
 }
 
 cudaError_t launch_router_bwd(const RouterBwdArgs& a, bool bf16, cudaStream_t st) {
   if (a.T == 0) return cudaSuccess;
-  const unsigned blocks = loss_blocks(a.T, a.E, 8);
+  const unsigned blocks = loss_blocks(a.T, a.E, RL_BLOCKS_PER_SM);
   const bool vec = rows_vectorised(a.logits, a.dlogits, a.E);
   count_launch();
   return by_group(a.E, [&](auto G) {

@@ -114,6 +114,18 @@ def test_shapes(T, E, k, bf16):
     _run(rng.normal(size=(T, E)) * 3, k, bf16=bf16)
 
 
+@pytest.mark.parametrize("T,E,k", [(300, 5, 5), (300, 8, 3), (200, 16, 16), (200, 29, 20), (200, 32, 32), (200, 60, 31),
+                                   (200, 128, 12), (200, 256, 32)])
+def test_same_bits_as_the_plain_router(T, E, k):
+    import torch
+    z = _device(np.random.default_rng(E + k).normal(size=(T, E)) * 2)
+    layer = _layer(T, E, k)
+    idx, prob, _ = layer.route_losses(z)
+    idx, prob = idx.clone(), prob.clone()
+    i2, p2 = layer.route(z)
+    assert torch.equal(idx, i2) and torch.equal(prob, p2)
+
+
 @pytest.mark.parametrize("name", ["tiny", "gpt_oss_20b", "qwen3_30b_ragged"])
 def test_workload_logits(name):
     cfg = get_config(name)
