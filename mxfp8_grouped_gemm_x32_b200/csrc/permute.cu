@@ -110,6 +110,82 @@ __global__ void __launch_bounds__(PB) perm_scatter_kernel(const int32_t* __restr
   }
 }
 
+// All passes at once for at most PB slots (a decoding batch), in one CTA: the
+// same results from one launch instead of five (two fills, histogram, scan,
+// scatter), whose launches would take longer than their work: 8 slots of 128
+// experts took 21.5 us between events, now 8.0 (events alone: 3).
+__global__ void __launch_bounds__(PB) perm_small_kernel(const int32_t* __restrict__ idx,
+                                                        const float* __restrict__ prob, int32_t R, int32_t E,
+                                                        int64_t rows_cap, int32_t* __restrict__ split,
+                                                        int32_t* __restrict__ offs, int32_t* __restrict__ slot_to_row,
+                                                        int32_t* __restrict__ row_to_slot,
+                                                        float* __restrict__ prob_perm) {
+  extern __shared__ int wcnt[];  // [32 warps][E]: counts, then first ranks; then [E + 1] group offsets
+  __shared__ int wsum[MOE_MAX_EXPERTS / 32];
+  int* goff = wcnt + 32 * E;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int32_t e = -1;
+  if (tid < R) {
+    e = idx[tid];
+    if (!id_ok(e, E)) {
+      set_status(MOE_ERR_DEVICE_INDEX);
+      e = -1;
+    }
+  }
+  for (int i = tid; i < 32 * E; i += PB) wcnt[i] = 0;
+  for (int64_t i = tid; i < rows_cap; i += PB) {
+    row_to_slot[i] = -1;
+    prob_perm[i] = 0.0f;
+  }
+  __syncthreads();
+  const uint32_t mask = __match_any_sync(0xFFFFFFFFu, e);
+  const uint32_t lrank = __popc(mask & ((1u << lane) - 1u));
+  if (e >= 0 && lrank == 0) wcnt[warp * E + e] = __popc(mask);
+  __syncthreads();
+  // thread x: expert x's slots before each warp's, its total and its padded rows
+  int32_t total = 0, padded = 0;
+  if (tid < MOE_MAX_EXPERTS) {
+    if (tid < E) {
+      for (int w = 0; w < 32; ++w) {
+        const int32_t c = wcnt[w * E + tid];
+        wcnt[w * E + tid] = total;
+        total += c;
+      }
+      split[tid] = total;
+      padded = (total + 127) / 128 * 128;
+    }
+    int32_t incl = padded;  // inclusive scan over the warp's experts
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    padded = incl - padded;  // rows of the warp's experts before this one
+    total = incl;
+  }
+  __syncthreads();
+  if (tid < MOE_MAX_EXPERTS) {
+    int32_t before = 0;
+    for (int w = 0; w < warp; ++w) before += wsum[w];
+    if (tid < E) {
+      offs[tid] = goff[tid] = before + padded;
+      if (tid == E - 1) offs[E] = before + total;
+    }
+  }
+  __syncthreads();
+  if (tid < R) {
+    if (e < 0) {
+      slot_to_row[tid] = -1;
+    } else {
+      const int32_t row = goff[e] + wcnt[warp * E + e] + int32_t(lrank);
+      slot_to_row[tid] = row;
+      row_to_slot[row] = tid;
+      prob_perm[row] = prob[tid];
+    }
+  }
+}
+
 // out[t] = sum_j y[row(t, j)], fp32 sum in ascending j, 8 columns per thread;
 // row(t, j) = t*k + j (rows in slot order) or slot_to_row[t*k + j] (rows in
 // permuted order).  FMT: y holds bf16 rows (COMBINE_BF16), fp32 rows
@@ -175,6 +251,12 @@ cudaError_t launch_permute_index(const int32_t* idx, const float* prob, int64_t 
                                  int64_t rows_cap, int32_t* split, int32_t* offs,
                                  int32_t* row_to_slot, int32_t* slot_to_row, float* prob_perm,
                                  void* ws, cudaStream_t st) {
+  if (R > 0 && R <= PB) {
+    perm_small_kernel<<<1, PB, 33 * E * sizeof(int), st>>>(idx, prob, int32_t(R), E, rows_cap, split, offs,
+                                                           slot_to_row, row_to_slot, prob_perm);
+    count_launch();
+    return cudaGetLastError();
+  }
   cudaError_t err = cudaMemsetAsync(row_to_slot, 0xFF, size_t(rows_cap) * 4, st);
   if (err != cudaSuccess) return err;
   err = cudaMemsetAsync(prob_perm, 0, size_t(rows_cap) * 4, st);

@@ -105,6 +105,12 @@ def on_device(dev: torch.device):
     return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
+# the raw handle of a device's current stream; the public call builds a Stream
+# object first, which takes longer (3 us) than a small kernel's launch
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class GroupedMLP:
     """One layer: T tokens, hidden H, intermediate I, E experts, top-k.
 
@@ -185,13 +191,14 @@ class GroupedMLP:
 
     def permute_index(self, topk_idx: torch.Tensor, topk_prob: torch.Tensor) -> None:
         """Routing outputs of the permutation only (no quantisation of x):
-        what the BF16 forward needs."""
+        what the BF16, per-tensor FP8 and MXFP4 forwards need."""
         check_tensor(topk_idx, "topk_idx", torch.int32, (self.T, self.k), self.dev)
         check_tensor(topk_prob, "topk_prob", torch.float32, (self.T, self.k), self.dev)
-        lib.moe_permute(0, topk_idx.data_ptr(), topk_prob.data_ptr(), self.T, self.H, self.k, self.E, self.rows_cap,
-                        _ptr(self.split_sizes), _ptr(self.group_offsets), _ptr(self.row_to_slot),
-                        _ptr(self.slot_to_row), _ptr(self.prob_perm), 0, 0, 0, 0, _ptr(self.ws_perm),
-                        self.ws_perm_bytes, self._stream())
+        with on_device(self.dev):
+            lib.moe_permute(0, topk_idx.data_ptr(), topk_prob.data_ptr(), self.T, self.H, self.k, self.E,
+                            self.rows_cap, _ptr(self.split_sizes), _ptr(self.group_offsets), _ptr(self.row_to_slot),
+                            _ptr(self.slot_to_row), _ptr(self.prob_perm), 0, 0, 0, 0, _ptr(self.ws_perm),
+                            self.ws_perm_bytes, self._stream())
 
     def forward_bf16(self, x: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor) -> torch.Tensor:
         """BF16 recipe forward (moe_grouped_mlp_fwd_bf16) on the routing of
@@ -399,9 +406,8 @@ class GroupedMLP:
         guard > 0; always empty otherwise)."""
         return self._alloc.check()
 
-    @staticmethod
-    def _stream() -> int:
-        return torch.cuda.current_stream().cuda_stream
+    def _stream(self) -> int:
+        return _raw_stream(self.dev.index)
 
     def quantize_weights(self, w1: torch.Tensor, w2: torch.Tensor) -> None:
         """w1 bf16 [E, 2I, H] (gate rows first), w2 bf16 [E, H, I]."""

@@ -8,7 +8,12 @@ from __future__ import annotations
 import torch
 
 from . import lib
-from .layer import _DTYPES, check_tensor, on_device
+from .layer import _DTYPES, _raw_stream, check_tensor, on_device
+
+
+def _scale_bytes(groups: int, rows: int, K: int) -> int:
+    """lib.moe_mx_scale_bytes without the call into the library."""
+    return groups * -(-rows // 128) * -(-K // 128) * 512
 
 
 def _extent(shape):
@@ -37,12 +42,13 @@ def quantize(x: torch.Tensor):
     groups, rows, K = _extent(x.shape)
     if K % 32:
         raise ValueError(f"x: the last axis must be a multiple of 32, got {K}")
-    check_tensor(x, "x", x.dtype, x.shape, x.device)
+    if not x.is_contiguous():
+        raise ValueError("x: must be contiguous")
     with on_device(x.device):
         codes = torch.empty(*x.shape[:-1], K // 2, dtype=torch.uint8, device=x.device)
-        scales = torch.empty(lib.moe_mx_scale_bytes(groups, rows, K), dtype=torch.uint8, device=x.device)
+        scales = torch.empty(_scale_bytes(groups, rows, K), dtype=torch.uint8, device=x.device)
         lib.moe_mlp_quantize_mxfp4(x.data_ptr(), dt, groups, rows, K, codes.data_ptr(), scales.data_ptr(),
-                                   torch.cuda.current_stream().cuda_stream)
+                                   _raw_stream(x.device.index))
     return codes, scales
 
 
@@ -59,10 +65,13 @@ def dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = t
     groups, rows, half = _extent(codes.shape)
     if half % 16:
         raise ValueError(f"codes: the last axis must be a multiple of 16, got {half}")
-    check_tensor(codes, "codes", torch.uint8, codes.shape, codes.device)
-    check_tensor(scales, "scales", torch.uint8, (lib.moe_mx_scale_bytes(groups, rows, 2 * half),), codes.device)
+    if codes.dtype != torch.uint8:
+        raise TypeError(f"codes: expected torch.uint8, got {codes.dtype}")
+    if not codes.is_contiguous():
+        raise ValueError("codes: must be contiguous")
+    check_tensor(scales, "scales", torch.uint8, (_scale_bytes(groups, rows, 2 * half),), codes.device)
     with on_device(codes.device):
         out = torch.empty(*codes.shape[:-1], 2 * half, dtype=dtype, device=codes.device)
         lib.moe_mlp_dequantize_mxfp4(codes.data_ptr(), scales.data_ptr(), groups, rows, 2 * half, dt, out.data_ptr(),
-                                     torch.cuda.current_stream().cuda_stream)
+                                     _raw_stream(codes.device.index))
     return out

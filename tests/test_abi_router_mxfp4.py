@@ -99,6 +99,12 @@ def test_forward_call():
     assert lib.moe_workspace_size(lib.MOE_OP_FWD_MXFP4, 64, 2, 4, 0, 512) == -1
 
 
+@pytest.mark.parametrize("g,r,k", [(1, 1, 32), (3, 128, 128), (2, 129, 2880), (0, 5, 64), (7, 0, 96)])
+def test_scale_bytes_of_the_python_layer(g, r, k):
+    from mxfp8_grouped_gemm_x32_b200 import mxfp4
+    assert mxfp4._scale_bytes(g, r, k) == lib.moe_mx_scale_bytes(g, r, k)
+
+
 def test_half_the_bytes_of_the_mxfp8_recipe():
     """Codes of 4 bits: a layer's MXFP4 weights take half of its MXFP8 ones."""
     E, H, I = 8, 4096, 14336
