@@ -460,40 +460,56 @@ moe_status_t moe_router_bwd(const void* logits, int32_t logits_dtype, int32_t T,
  * the last axis, the same blocked scale layout, moe_mx_scale_bytes) with
  * 4-bit E2M1 elements: +-{0, .5, 1, 1.5, 2, 3, 4, 6}.
  *   src   [groups][rows][cols] bf16 or fp32 (dtype), contiguous.
- *   q     uint8 [groups][rows][cols/2]: element 2i in the low four bits of byte
- *         i, element 2i+1 in the high four.
+ *   q     uint8 [groups][rows], rows ldq bytes apart (ldq >= cols/2, a multiple
+ *         of 16): element 2i in the low four bits of byte i, element 2i+1 in the
+ *         high four.  The layer's GEMMs read rows that start on 128-byte lines
+ *         (ldq a multiple of 128) nearly twice as fast as others.
  *   sf    blocked scales (groups, rows, cols); bytes of no block are 0.
  * Scale rule: s = smallest integer with amax/2^s <= 6, clamped to [-127, 127];
  * all-zero block -> s = -127; block with NaN/Inf -> scale byte 0xFF (its codes
  * say nothing).  Codes: E2M1(v * 2^-s), round to nearest even.
  * Needs cols % 32 == 0 and groups*rows*cols < 2^34 - 2^27 (MOE_ERR_UNSUPPORTED
- * otherwise), pointers 16-byte aligned.  Codes in rows order and scales in
- * plain order from elsewhere (a checkpoint in 4 bits) are taken as they are,
- * the scales after moe_mx_scales_to_blocked. */
+ * otherwise), pointers 16-byte aligned. */
 moe_status_t moe_mlp_quantize_mxfp4(const void* src, int32_t dtype, int32_t groups, int64_t rows, int64_t cols,
-                                    uint8_t* q, uint8_t* sf, moe_stream_t stream);
+                                    uint8_t* q, int64_t ldq, uint8_t* sf, moe_stream_t stream);
 
 /* The values that codes and scales stand for: dst [groups][rows][cols], bf16 or
  * fp32 (dtype), code * 2^(b - 127), NaN for scale byte 0xFF; exact in both
  * types, but for values past them: a |max| above 1.75 * 2^127 rounds to 2^128,
  * which both types hold as infinity. */
-moe_status_t moe_mlp_dequantize_mxfp4(const uint8_t* q, const uint8_t* sf, int32_t groups, int64_t rows, int64_t cols,
-                                      int32_t dtype, void* dst, moe_stream_t stream);
+moe_status_t moe_mlp_dequantize_mxfp4(const uint8_t* q, int64_t ldq, const uint8_t* sf, int32_t groups, int64_t rows,
+                                      int64_t cols, int32_t dtype, void* dst, moe_stream_t stream);
+
+/* Weight scales for moe_grouped_mlp_fwd_mxfp4, in the order its GEMMs read them (done
+ * once per set of weights): tiles of 192 output columns by 256 values of K, 1536
+ * bytes each.  plain: the ordinary order, row-major [matrices][n][k/32] with ld bytes
+ * between rows, one E8M0 byte per 32 values (moe_mx_scales_from_blocked gives it
+ * for what moe_mlp_quantize_mxfp4 wrote; a checkpoint in 4 bits has it).
+ *   gate_up = 1: W_gate_up, 2E matrices of n = I rows (gate and up in turn), k = H;
+ *   gate_up = 0: W_down, E matrices of n = H rows, k = I.
+ *   tiled   moe_mxfp4_tiled_scale_bytes(E, n, k, gate_up) bytes (-1 on invalid
+ *           sizes), 16-byte aligned.
+ * Needs k % 32 == 0 and ld >= k/32 (MOE_ERR_INVALID otherwise). */
+int64_t moe_mxfp4_tiled_scale_bytes(int32_t E, int32_t n, int64_t k, int32_t gate_up);
+moe_status_t moe_mxfp4_tile_scales(const uint8_t* plain, int32_t E, int32_t n, int64_t k, int64_t ld, int32_t gate_up,
+                                   uint8_t* tiled, moe_stream_t stream);
 
 /* MXFP4 recipe forward (serving): moe_grouped_mlp_fwd with 4-bit weights and
  * activations on the kind::mxf4 tensor cores (fp32 accumulation).  x is
  * quantised along H, h = prob * silu(gate) * up (fp32) along I; out[t] =
  * sum_j y[row(t, j)] (y kept in 24 bits as in moe_grouped_mlp_fwd, fp32 sum in
  * ascending j, one bf16 rounding).  No backward: the recipe trains in MXFP8.
- *   w1q, w1sf  MXFP4 tensor (2E, I, H): W_gate_up [E][2I][H], gate rows first.
- *   w2q, w2sf  MXFP4 tensor (E, H, I): W_down.
+ *   w1q, w1sf  codes of W_gate_up [E][2I][H], gate rows first, ld1 bytes between
+ *              rows (as ldq above), and its tiled scales (gate_up = 1).
+ *   w2q, w2sf  codes of W_down [E][H][I], ld2 bytes between rows, and its tiled
+ *              scales (gate_up = 0).
  *   routing    from moe_permute (xq may be NULL there).
  *   x          bf16 [T][H];  out bf16 [T][H].
  *   workspace  >= moe_workspace_size(MOE_OP_FWD_MXFP4, T, k, E, H, I), 256-byte
  *              aligned.
  * Limits as moe_grouped_mlp_fwd, and T*H < 2^34 - 2^27. */
-moe_status_t moe_grouped_mlp_fwd_mxfp4(const uint8_t* w1q, const uint8_t* w1sf, const uint8_t* w2q,
-                                       const uint8_t* w2sf, int32_t T, int32_t H, int32_t I, int32_t E, int32_t k,
+moe_status_t moe_grouped_mlp_fwd_mxfp4(const uint8_t* w1q, int64_t ld1, const uint8_t* w1sf, const uint8_t* w2q,
+                                       int64_t ld2, const uint8_t* w2sf, int32_t T, int32_t H, int32_t I, int32_t E, int32_t k,
                                        int64_t rows_cap, const int32_t* split_sizes, const int32_t* group_offsets,
                                        const int32_t* slot_to_row, const float* prob_perm, const void* x, void* out,
                                        void* workspace, size_t workspace_bytes, moe_stream_t stream);

@@ -119,9 +119,9 @@ struct FwdMxfp4Ws {
 };
 FwdMxfp4Ws carve_fwd_mxfp4(Carver& c, int64_t H, int64_t I, int64_t rows_cap) {
   FwdMxfp4Ws w{};
-  w.xq = c.take(rows_cap * (H / 2));
+  w.xq = c.take(rows_cap * mxfp4_pitch(H));
   w.xq_sf = c.take(mx_scale_bytes(1, rows_cap, H));
-  w.hq = c.take(rows_cap * (I / 2));
+  w.hq = c.take(rows_cap * mxfp4_pitch(I));
   w.hq_sf = c.take(mx_scale_bytes(1, rows_cap, I));
   w.y = c.take(rows_cap * H * 3);
   return w;
@@ -1065,38 +1065,56 @@ moe_status_t moe_router_bwd(const void* logits, int32_t logits_dtype, int32_t T,
 }
 
 moe_status_t moe_mlp_quantize_mxfp4(const void* src, int32_t dtype, int32_t groups, int64_t rows, int64_t cols,
-                                    uint8_t* q, uint8_t* sf, moe_stream_t stream) {
+                                    uint8_t* q, int64_t ldq, uint8_t* sf, moe_stream_t stream) {
   if (groups < 0 || rows < 0 || cols < 0 || (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16))
     return MOE_ERR_INVALID;
   if (cols % 32) return MOE_ERR_UNSUPPORTED;
   if (groups == 0 || rows == 0 || cols == 0) return MOE_OK;
   if (!src || !q || !sf || !al16(src) || !al16(q) || !al16(sf)) return MOE_ERR_INVALID;
+  if (ldq < cols / 2 || ldq % 16) return MOE_ERR_INVALID;
   if (!mxfp4_size_ok(groups, rows, cols)) return MOE_ERR_UNSUPPORTED;
   if (!device_ok()) return MOE_ERR_NO_DEVICE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   TimeScope ts(st, "quant_mxfp4");
-  return cuda_status(launch_mxfp4_quant(Mxfp4Args{src, nullptr, q, sf, groups, rows, cols}, dtype == MOE_DTYPE_BF16,
+  return cuda_status(launch_mxfp4_quant(Mxfp4Args{src, nullptr, q, sf, groups, rows, cols, ldq}, dtype == MOE_DTYPE_BF16,
                                         st));
 }
 
-moe_status_t moe_mlp_dequantize_mxfp4(const uint8_t* q, const uint8_t* sf, int32_t groups, int64_t rows, int64_t cols,
-                                      int32_t dtype, void* dst, moe_stream_t stream) {
+moe_status_t moe_mlp_dequantize_mxfp4(const uint8_t* q, int64_t ldq, const uint8_t* sf, int32_t groups, int64_t rows,
+                                      int64_t cols, int32_t dtype, void* dst, moe_stream_t stream) {
   if (groups < 0 || rows < 0 || cols < 0 || (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16))
     return MOE_ERR_INVALID;
   if (cols % 32) return MOE_ERR_UNSUPPORTED;
   if (groups == 0 || rows == 0 || cols == 0) return MOE_OK;
   if (!q || !sf || !dst || !al16(q) || !al16(sf) || !al16(dst)) return MOE_ERR_INVALID;
+  if (ldq < cols / 2 || ldq % 16) return MOE_ERR_INVALID;
   if (!mxfp4_size_ok(groups, rows, cols)) return MOE_ERR_UNSUPPORTED;
   if (!device_ok()) return MOE_ERR_NO_DEVICE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   TimeScope ts(st, "dequant_mxfp4");
   return cuda_status(launch_mxfp4_dequant(
-      Mxfp4Args{nullptr, dst, const_cast<uint8_t*>(q), const_cast<uint8_t*>(sf), groups, rows, cols},
+      Mxfp4Args{nullptr, dst, const_cast<uint8_t*>(q), const_cast<uint8_t*>(sf), groups, rows, cols, ldq},
       dtype == MOE_DTYPE_BF16, st));
 }
 
-moe_status_t moe_grouped_mlp_fwd_mxfp4(const uint8_t* w1q, const uint8_t* w1sf, const uint8_t* w2q,
-                                       const uint8_t* w2sf, int32_t T, int32_t H, int32_t I, int32_t E, int32_t k,
+int64_t moe_mxfp4_tiled_scale_bytes(int32_t E, int32_t n, int64_t k, int32_t gate_up) {
+  if (E < 0 || n < 0 || k < 0 || k % 32 || (gate_up != 0 && gate_up != 1)) return -1;
+  return mxfp4_tiled_scale_bytes(E, n, k, gate_up != 0);
+}
+
+moe_status_t moe_mxfp4_tile_scales(const uint8_t* plain, int32_t E, int32_t n, int64_t k, int64_t ld, int32_t gate_up,
+                                   uint8_t* tiled, moe_stream_t stream) {
+  const int64_t bytes = moe_mxfp4_tiled_scale_bytes(E, n, k, gate_up);
+  if (bytes < 0 || ld < k / 32) return MOE_ERR_INVALID;
+  if (bytes == 0) return MOE_OK;
+  if (!plain || !tiled || !al16(tiled)) return MOE_ERR_INVALID;
+  if (!device_ok()) return MOE_ERR_NO_DEVICE;
+  return cuda_status(launch_mxfp4_tile_scales(plain, ld, E, n, k, gate_up != 0, tiled,
+                                              reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_grouped_mlp_fwd_mxfp4(const uint8_t* w1q, int64_t ld1, const uint8_t* w1sf, const uint8_t* w2q,
+                                       int64_t ld2, const uint8_t* w2sf, int32_t T, int32_t H, int32_t I, int32_t E, int32_t k,
                                        int64_t rows_cap, const int32_t* split_sizes, const int32_t* group_offsets,
                                        const int32_t* slot_to_row, const float* prob_perm, const void* x, void* out,
                                        void* workspace, size_t workspace_bytes, moe_stream_t stream) {
@@ -1109,6 +1127,7 @@ moe_status_t moe_grouped_mlp_fwd_mxfp4(const uint8_t* w1q, const uint8_t* w1sf, 
   for (const void* p : {(const void*)w1q, (const void*)w1sf, (const void*)w2q, (const void*)w2sf, x,
                         (const void*)out})
     if (!al16(p)) return MOE_ERR_INVALID;
+  if (ld1 < H / 2 || ld1 % 16 || ld2 < I / 2 || ld2 % 16) return MOE_ERR_INVALID;
   Carver c{static_cast<uint8_t*>(workspace)};
   const FwdMxfp4Ws w = carve_fwd_mxfp4(c, H, I, rows_cap);
   if (!workspace || !al256(workspace) || int64_t(workspace_bytes) < c.off) return MOE_ERR_WORKSPACE;
@@ -1126,12 +1145,12 @@ moe_status_t moe_grouped_mlp_fwd_mxfp4(const uint8_t* w1q, const uint8_t* w1sf, 
   {
     TimeScope ts(st, "gemm_gate_up_swiglu_mxfp4");
     g.N = I; g.K = H; g.sfa = w.xq_sf; g.sfb = w1sf; g.prob = prob_perm; g.q_out = w.hq; g.sf_out = w.hq_sf;
-    if (launch_grouped_gemm_mxfp4(EPI4_SWIGLU, w.xq, rows_cap, w1q, g, R, st) != cudaSuccess) return MOE_ERR_CUDA;
+    if (launch_grouped_gemm_mxfp4(EPI4_SWIGLU, w.xq, rows_cap, w1q, ld1, g, R, st) != cudaSuccess) return MOE_ERR_CUDA;
   }
   {
     TimeScope ts(st, "gemm_down_mxfp4");
     g.N = H; g.K = I; g.sfa = w.hq_sf; g.sfb = w2sf; g.out = w.y;
-    if (launch_grouped_gemm_mxfp4(EPI4_F24_ROWS, w.hq, rows_cap, w2q, g, R, st) != cudaSuccess) return MOE_ERR_CUDA;
+    if (launch_grouped_gemm_mxfp4(EPI4_F24_ROWS, w.hq, rows_cap, w2q, ld2, g, R, st) != cudaSuccess) return MOE_ERR_CUDA;
   }
   TimeScope ts(st, "combine");
   return cuda_status(launch_combine(w.y, COMBINE_F24, slot_to_row, T, k, H, out, st));

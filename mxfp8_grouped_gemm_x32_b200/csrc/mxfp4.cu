@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(Q4_THREADS) mxfp4_quant_kernel(const Mxfp4Args
         sb |= __shfl_xor_sync(0xFFFFFFFFu, sb, 8);
       }
       if (i >= n) continue;
-      reinterpret_cast<uint32_t*>(a.q)[i] = w;
+      *reinterpret_cast<uint32_t*>(a.q + int64_t(rr) * a.ldq + 4 * u) = w;
       if (u & (WORDS ? 15u : 3u)) continue;
       const uint32_t g = fastdiv(rr, a.rows_div), r = rr - g * rows, kb = u >> 2;
       uint8_t* p = a.sf + sf_offset(g, r, kb, RT, KT);
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(Q4_THREADS) mxfp4_dequant_kernel(const Mxfp4Ar
       if (i < n) {
         const uint32_t rr = fastdiv(i, a.units_div), u = i - rr * U;
         const uint32_t g = fastdiv(rr, a.rows_div), r = rr - g * rows;
-        w[j] = __ldg(reinterpret_cast<const uint32_t*>(a.q) + i);
+        w[j] = __ldg(reinterpret_cast<const uint32_t*>(a.q + int64_t(rr) * a.ldq + 4 * u));
         sb[j] = __ldg(a.sf + sf_offset(g, r, u >> 2, RT, KT));
       }
     }
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(Q4_THREADS) mxfp4_quant_scatter_kernel(const M
         for (int x = 0; x < 4; ++x) {
           if (rw[x] < 0) continue;  // past k, or a slot whose expert id was rejected
           const int64_t r = rw[x];
-          *reinterpret_cast<uint32_t*>(a.q + r * (a.H / 2) + u * 4) = w;
+          *reinterpret_cast<uint32_t*>(a.q + r * mxfp4_pitch(a.H) + u * 4) = w;
           if (lead) {
             a.sf[sf_offset(0, r, kb, 0, KT)] = uint8_t(sb);
             if (last)

@@ -30,15 +30,22 @@ __device__ __forceinline__ uint32_t pack8_e2m1(const float* f) {
   return r;
 }
 
+// Bytes between rows of the codes that the library lays out itself: whole 128-byte
+// lines, so that no 128-byte box row of a TMA load straddles two (2880 values,
+// 1440 bytes a row: the GEMMs' loads ran at 38 bytes per cycle and SM, against 71
+// for aligned rows).
+__host__ __device__ __forceinline__ int64_t mxfp4_pitch(int64_t K) { return (K / 2 + 127) / 128 * 128; }
+
 // Source of the quantiser / destination of the dequantiser: `rows` rows of K
-// values per group, contiguous; codes [groups][rows][K/2], scales blocked.
+// values per group, contiguous; codes [groups][rows], rows `ldq` bytes apart,
+// scales blocked.
 struct Mxfp4Args {
   const void* src;
   void* dst;
   uint8_t* q;
   uint8_t* sf;
   int32_t groups;
-  int64_t rows, K;
+  int64_t rows, K, ldq;
   FastDiv units_div, rows_div;  // K / 8 and rows (set by the launcher)
 };
 // units of 8 values have to be fewer than this (32-bit indices)
@@ -53,11 +60,19 @@ struct Mxfp4ScatterArgs {
   const uint8_t* src;
   int32_t T, H, k;
   const int32_t* slot_to_row;
-  uint8_t* q;   // [rows_cap][H/2]
+  uint8_t* q;   // [rows_cap][H/2], mxfp4_pitch(H) bytes a row
   uint8_t* sf;  // blocked (1, rows_cap, H)
   FastDiv units_div;  // H / 8 (set by the launcher)
 };
 cudaError_t launch_mxfp4_quant_scatter(Mxfp4ScatterArgs a, cudaStream_t st);
+
+// Weight scales in the order the GEMM's tiles read them: per expert, column tile and
+// K tile of 256 values 48 bytes for each of 32 lanes, one copy a K tile (the
+// blocked order takes up to four, and twice the shared-memory reads).
+constexpr int MXFP4_TILE_SF = 32 * 48;
+int64_t mxfp4_tiled_scale_bytes(int64_t E, int64_t N, int64_t K, bool gate_up);
+cudaError_t launch_mxfp4_tile_scales(const uint8_t* plain, int64_t ld, int32_t E, int32_t N, int64_t K, bool gate_up,
+                                     uint8_t* tiled, cudaStream_t st);
 
 // Grouped GEMM on MXFP4 operands over the permuted rows (see gemm_mxfp4.cu).
 enum Mxfp4Epi : int {
@@ -66,17 +81,19 @@ enum Mxfp4Epi : int {
 };
 struct Gemm4Args {
   int32_t E, N, K;      // N: output columns (EPI4_SWIGLU: I); K: contraction length, a multiple of 32
-  int32_t a_box;        // rows of the A tensor map's box
   const int32_t* group_offsets;
   const int32_t* split_sizes;
   const uint8_t* sfa;   // blocked (1, rows_cap, K)
-  const uint8_t* sfb;   // blocked (E, N, K); EPI4_SWIGLU: (2E, I, K)
+  const uint8_t* sfb;   // tiled (see mxfp4_tiled_scale_bytes)
   const float* prob;
   uint8_t* out;         // EPI4_F24_ROWS: f24 rows [rows_cap][N]
-  uint8_t* q_out;       // EPI4_SWIGLU: h codes [rows_cap][N/2]
+  uint8_t* q_out;       // EPI4_SWIGLU: h codes [rows_cap][N/2], mxfp4_pitch(N) bytes a row
   uint8_t* sf_out;      // EPI4_SWIGLU: blocked (1, rows_cap, N)
 };
+// a_codes: permuted rows, mxfp4_pitch(K) bytes apart; b_codes: rows b_pitch bytes
+// apart.  max_rows: routed rows T*k -- no more 128-row tiles than experts or rows
+// are occupied.
 cudaError_t launch_grouped_gemm_mxfp4(int epi, const uint8_t* a_codes, int64_t rows_cap, const uint8_t* b_codes,
-                                      Gemm4Args a, int64_t max_rows, cudaStream_t st);
+                                      int64_t b_pitch, Gemm4Args a, int64_t max_rows, cudaStream_t st);
 
 }  // namespace moe

@@ -345,11 +345,13 @@ class GroupedMLP:
 
     def _mxfp4_weights(self):
         if self.w1q4 is None:
-            u8, sb, E, H, I = self._alloc.raw, lib.moe_mx_scale_bytes, self.E, self.H, self.I
-            self.w1sf4 = u8(sb(2 * E, I, H), "w1sf4")
-            self.w2sf4 = u8(sb(E, H, I), "w2sf4")
-            self.w2q4 = u8(E * H * I // 2, "w2q4")
-            self.w1q4 = u8(E * I * H, "w1q4")
+            u8, E, H, I = self._alloc.raw, self.E, self.H, self.I
+            self.w1sf4 = u8(lib.moe_mxfp4_tiled_scale_bytes(E, I, H, 1), "w1sf4")
+            self.w2sf4 = u8(lib.moe_mxfp4_tiled_scale_bytes(E, H, I, 0), "w2sf4")
+            # rows of codes start on 128-byte lines
+            self.ld1_4, self.ld2_4 = (H // 2 + 127) // 128 * 128, (I // 2 + 127) // 128 * 128
+            self.w2q4 = u8(E * H * self.ld2_4, "w2q4")
+            self.w1q4 = u8(E * 2 * I * self.ld1_4, "w1q4")
 
     def quantize_weights_mxfp4(self, w1: torch.Tensor, w2: torch.Tensor) -> None:
         """w1 bf16 [E, 2I, H] (gate rows first), w2 bf16 [E, H, I] -> this
@@ -360,8 +362,14 @@ class GroupedMLP:
         self._mxfp4_weights()
         with on_device(self.dev):
             s, bf = self._stream(), lib.MOE_DTYPE_BF16
-            lib.moe_mlp_quantize_mxfp4(w1.data_ptr(), bf, 2 * E, I, H, _ptr(self.w1q4), _ptr(self.w1sf4), s)
-            lib.moe_mlp_quantize_mxfp4(w2.data_ptr(), bf, E, H, I, _ptr(self.w2q4), _ptr(self.w2sf4), s)
+            for w, matrices, n, k, q, ld, sf, gate_up in ((w1, 2 * E, I, H, self.w1q4, self.ld1_4, self.w1sf4, 1),
+                                                          (w2, E, H, I, self.w2q4, self.ld2_4, self.w2sf4, 0)):
+                # the quantiser's blocked scales, in row order, in the GEMMs' order
+                blocked = torch.empty(lib.moe_mx_scale_bytes(matrices, n, k), dtype=torch.uint8, device=self.dev)
+                plain = torch.empty(matrices * n * (k // 32), dtype=torch.uint8, device=self.dev)
+                lib.moe_mlp_quantize_mxfp4(w.data_ptr(), bf, matrices, n, k, _ptr(q), ld, _ptr(blocked), s)
+                lib.moe_mx_scales_from_blocked(_ptr(blocked), matrices, n, k, _ptr(plain), k // 32, s)
+                lib.moe_mxfp4_tile_scales(_ptr(plain), E, n, k, k // 32, gate_up, _ptr(sf), s)
 
     def load_weights_mxfp4(self, w1_codes: torch.Tensor, w1_scales: torch.Tensor, w2_codes: torch.Tensor,
                            w2_scales: torch.Tensor) -> None:
@@ -376,11 +384,11 @@ class GroupedMLP:
         check_tensor(w2_scales, "w2_scales", torch.uint8, (E, H, I // 32), self.dev)
         self._mxfp4_weights()
         with on_device(self.dev):
-            self.w1q4[: w1_codes.numel()].copy_(w1_codes.view(-1))
-            self.w2q4[: w2_codes.numel()].copy_(w2_codes.view(-1))
+            self.w1q4[: E * 2 * I * self.ld1_4].view(E, 2 * I, -1)[..., : H // 2].copy_(w1_codes)
+            self.w2q4[: E * H * self.ld2_4].view(E, H, -1)[..., : I // 2].copy_(w2_codes)
             s = self._stream()
-            lib.moe_mx_scales_to_blocked(_ptr(w1_scales), 2 * E, I, H, H // 32, _ptr(self.w1sf4), s)
-            lib.moe_mx_scales_to_blocked(_ptr(w2_scales), E, H, I, I // 32, _ptr(self.w2sf4), s)
+            lib.moe_mxfp4_tile_scales(_ptr(w1_scales), E, I, H, H // 32, 1, _ptr(self.w1sf4), s)
+            lib.moe_mxfp4_tile_scales(_ptr(w2_scales), E, H, I, I // 32, 0, _ptr(self.w2sf4), s)
 
     def forward_mxfp4(self, x: torch.Tensor) -> torch.Tensor:
         """MXFP4 recipe forward (moe_grouped_mlp_fwd_mxfp4) on the routing of
@@ -394,11 +402,11 @@ class GroupedMLP:
             self.ws_mxfp4_bytes = lib.moe_workspace_size(lib.MOE_OP_FWD_MXFP4, self.T, self.k, E, H, I)
             self.ws_mxfp4 = self._alloc.raw(self.ws_mxfp4_bytes, "ws_mxfp4")
         with on_device(self.dev):
-            lib.moe_grouped_mlp_fwd_mxfp4(_ptr(self.w1q4), _ptr(self.w1sf4), _ptr(self.w2q4), _ptr(self.w2sf4), self.T,
-                                          H, I, E, self.k, self.rows_cap, _ptr(self.split_sizes),
-                                          _ptr(self.group_offsets), _ptr(self.slot_to_row), _ptr(self.prob_perm),
-                                          x.data_ptr(), _ptr(self.out), _ptr(self.ws_mxfp4), self.ws_mxfp4_bytes,
-                                          self._stream())
+            lib.moe_grouped_mlp_fwd_mxfp4(_ptr(self.w1q4), self.ld1_4, _ptr(self.w1sf4), _ptr(self.w2q4), self.ld2_4,
+                                          _ptr(self.w2sf4), self.T, H, I, E, self.k, self.rows_cap,
+                                          _ptr(self.split_sizes), _ptr(self.group_offsets), _ptr(self.slot_to_row),
+                                          _ptr(self.prob_perm), x.data_ptr(), _ptr(self.out), _ptr(self.ws_mxfp4),
+                                          self.ws_mxfp4_bytes, self._stream())
         return self.out
 
     def check_guards(self):

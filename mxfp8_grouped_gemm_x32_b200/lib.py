@@ -43,7 +43,7 @@ EXPORTED = [
     "moe_router_topk", "moe_mx_scales_to_blocked", "moe_mx_scales_from_blocked", "moe_route_permute",
     "moe_grouped_mlp_fwd_bf16", "moe_grouped_mlp_fwd_fp8_tensor", "moe_grouped_mlp_bwd_bf16",
     "moe_grouped_mlp_bwd_fp8_tensor", "moe_router_losses", "moe_router_bwd", "moe_mlp_quantize_mxfp4",
-    "moe_mlp_dequantize_mxfp4", "moe_grouped_mlp_fwd_mxfp4",
+    "moe_mlp_dequantize_mxfp4", "moe_grouped_mlp_fwd_mxfp4", "moe_mxfp4_tiled_scale_bytes", "moe_mxfp4_tile_scales",
 ]
 MOE_DTYPE_F32, MOE_DTYPE_BF16 = 0, 1
 
@@ -99,10 +99,12 @@ _decl("moe_grouped_mlp_bwd_fp8_tensor", _I32, _P, _P, _I32, _I32, _I32, _I32, _I
       _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P)
 _decl("moe_router_losses", _I32, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P)
 _decl("moe_router_bwd", _I32, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P)
-_decl("moe_mlp_quantize_mxfp4", _I32, _P, _I32, _I32, _I64, _I64, _P, _P, _P)
-_decl("moe_mlp_dequantize_mxfp4", _I32, _P, _P, _I32, _I64, _I64, _I32, _P, _P)
-_decl("moe_grouped_mlp_fwd_mxfp4", _I32, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _I64, _P, _P, _P, _P, _P, _P,
-      _P, _SZ, _P)
+_decl("moe_mlp_quantize_mxfp4", _I32, _P, _I32, _I32, _I64, _I64, _P, _I64, _P, _P)
+_decl("moe_mlp_dequantize_mxfp4", _I32, _P, _I64, _P, _I32, _I64, _I64, _I32, _P, _P)
+_decl("moe_mxfp4_tiled_scale_bytes", _I64, _I32, _I32, _I64, _I32)
+_decl("moe_mxfp4_tile_scales", _I32, _P, _I32, _I32, _I64, _I64, _I32, _P, _P)
+_decl("moe_grouped_mlp_fwd_mxfp4", _I32, _P, _I64, _P, _P, _I64, _P, _I32, _I32, _I32, _I32, _I32, _I64, _P, _P, _P,
+      _P, _P, _P, _P, _SZ, _P)
 _decl("moe_get_device_status", _I32, _P)
 _decl("moe_status_string", ctypes.c_char_p, _I32)
 _decl("moe_launch_count", _I64, _I32)
@@ -247,19 +249,28 @@ def moe_router_bwd(logits, logits_dtype, T, E, k, token_mask, topk_idx, topk_pro
         stream))
 
 
-def moe_mlp_quantize_mxfp4(src, dtype, groups, rows, cols, q, sf, stream=0):
-    _check("moe_mlp_quantize_mxfp4", _lib.moe_mlp_quantize_mxfp4(src, dtype, groups, rows, cols, q, sf, stream))
+def moe_mlp_quantize_mxfp4(src, dtype, groups, rows, cols, q, ldq, sf, stream=0):
+    _check("moe_mlp_quantize_mxfp4", _lib.moe_mlp_quantize_mxfp4(src, dtype, groups, rows, cols, q, ldq, sf, stream))
 
 
-def moe_mlp_dequantize_mxfp4(q, sf, groups, rows, cols, dtype, dst, stream=0):
-    _check("moe_mlp_dequantize_mxfp4", _lib.moe_mlp_dequantize_mxfp4(q, sf, groups, rows, cols, dtype, dst, stream))
+def moe_mlp_dequantize_mxfp4(q, ldq, sf, groups, rows, cols, dtype, dst, stream=0):
+    _check("moe_mlp_dequantize_mxfp4", _lib.moe_mlp_dequantize_mxfp4(q, ldq, sf, groups, rows, cols, dtype, dst,
+                                                                     stream))
 
 
-def moe_grouped_mlp_fwd_mxfp4(w1q, w1sf, w2q, w2sf, T, H, I, E, k, rows_cap, split_sizes, group_offsets, slot_to_row,
+def moe_mxfp4_tiled_scale_bytes(E: int, n: int, k: int, gate_up: int) -> int:
+    return _lib.moe_mxfp4_tiled_scale_bytes(E, n, k, gate_up)
+
+
+def moe_mxfp4_tile_scales(plain, E, n, k, ld, gate_up, tiled, stream=0):
+    _check("moe_mxfp4_tile_scales", _lib.moe_mxfp4_tile_scales(plain, E, n, k, ld, gate_up, tiled, stream))
+
+
+def moe_grouped_mlp_fwd_mxfp4(w1q, ld1, w1sf, w2q, ld2, w2sf, T, H, I, E, k, rows_cap, split_sizes, group_offsets, slot_to_row,
                               prob_perm, x, out, workspace, workspace_bytes, stream=0):
     _check("moe_grouped_mlp_fwd_mxfp4", _lib.moe_grouped_mlp_fwd_mxfp4(
-        w1q, w1sf, w2q, w2sf, T, H, I, E, k, rows_cap, split_sizes, group_offsets, slot_to_row, prob_perm, x, out,
-        workspace, workspace_bytes, stream))
+        w1q, ld1, w1sf, w2q, ld2, w2sf, T, H, I, E, k, rows_cap, split_sizes, group_offsets, slot_to_row, prob_perm, x,
+        out, workspace, workspace_bytes, stream))
 
 
 def moe_get_device_status(stream=0) -> int:

@@ -47,8 +47,8 @@ def quantize(x: torch.Tensor):
     with on_device(x.device):
         codes = torch.empty(*x.shape[:-1], K // 2, dtype=torch.uint8, device=x.device)
         scales = torch.empty(_scale_bytes(groups, rows, K), dtype=torch.uint8, device=x.device)
-        lib.moe_mlp_quantize_mxfp4(x.data_ptr(), dt, groups, rows, K, codes.data_ptr(), scales.data_ptr(),
-                                   _raw_stream(x.device.index))
+        lib.moe_mlp_quantize_mxfp4(x.data_ptr(), dt, groups, rows, K, codes.data_ptr(), K // 2,
+                                   scales.data_ptr(), _raw_stream(x.device.index))
     return codes, scales
 
 
@@ -72,6 +72,6 @@ def dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = t
     check_tensor(scales, "scales", torch.uint8, (_scale_bytes(groups, rows, 2 * half),), codes.device)
     with on_device(codes.device):
         out = torch.empty(*codes.shape[:-1], 2 * half, dtype=dtype, device=codes.device)
-        lib.moe_mlp_dequantize_mxfp4(codes.data_ptr(), scales.data_ptr(), groups, rows, 2 * half, dt, out.data_ptr(),
-                                     _raw_stream(codes.device.index))
+        lib.moe_mlp_dequantize_mxfp4(codes.data_ptr(), half, scales.data_ptr(), groups, rows, 2 * half, dt,
+                                     out.data_ptr(), _raw_stream(codes.device.index))
     return out

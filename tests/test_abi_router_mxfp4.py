@@ -31,18 +31,19 @@ def _bwd(**kw):
 
 
 def _quant(**kw):
-    return lib._lib.moe_mlp_quantize_mxfp4(*_args(dict(src=P, dt=1, groups=1, rows=4, cols=64, q=P, sf=P, st=None), kw))
+    return lib._lib.moe_mlp_quantize_mxfp4(*_args(dict(src=P, dt=1, groups=1, rows=4, cols=64, q=P, ldq=max(0, kw.get("cols", 64) // 2), sf=P,
+                                                       st=None), kw))
 
 
 def _dequant(**kw):
-    return lib._lib.moe_mlp_dequantize_mxfp4(*_args(dict(q=P, sf=P, groups=1, rows=4, cols=64, dt=1, dst=P, st=None),
-                                                    kw))
+    return lib._lib.moe_mlp_dequantize_mxfp4(*_args(dict(
+        q=P, ldq=max(0, kw.get("cols", 64) // 2), sf=P, groups=1, rows=4, cols=64, dt=1, dst=P, st=None), kw))
 
 
 def _fwd(**kw):
     T, k, E = kw.get("T", 64), kw.get("k", 2), kw.get("E", 4)
     return lib._lib.moe_grouped_mlp_fwd_mxfp4(*_args(dict(
-        w1q=P, w1sf=P, w2q=P, w2sf=P, T=64, H=256, I=512, E=4, k=2, cap=lib.moe_padded_rows(T, k, E), split=P, offs=P,
+        w1q=P, ld1=2048, w1sf=P, w2q=P, ld2=256, w2sf=P, T=64, H=256, I=512, E=4, k=2, cap=lib.moe_padded_rows(T, k, E), split=P, offs=P,
         s2r=P, prob=P, x=P, out=P, ws=P, wsb=BIG, st=None), kw))
 
 
@@ -75,6 +76,7 @@ def test_codec_calls(call, out):
     assert call(cols=48) == UNSUPPORTED
     for name in ("q", "sf", out):
         assert call(**{name: None}) == INVALID and call(**{name: M}) == INVALID
+    assert call(ldq=16) == INVALID and call(ldq=40) == INVALID and call(ldq=-32) == INVALID
     # sizes past 32-bit unit numbers, also those whose product would wrap
     assert call(rows=1 << 31, cols=64) == UNSUPPORTED
     assert call(groups=1 << 30, rows=1 << 30, cols=1 << 20) == UNSUPPORTED
@@ -93,6 +95,8 @@ def test_forward_call():
         assert _fwd(**kw) in (UNSUPPORTED, INVALID), kw
     assert _fwd(T=1 << 25, k=1, H=4096) == UNSUPPORTED
     assert _fwd(cap=lib.moe_padded_rows(64, 2, 4) - 128) == INVALID
+    for kw in (dict(ld1=112), dict(ld1=136), dict(ld2=240), dict(ld2=264), dict(ld1=0)):
+        assert _fwd(**kw) == INVALID, kw
     assert _fwd(cap=lib.moe_padded_rows(64, 2, 4) + 64) == INVALID
     need = lib.moe_workspace_size(lib.MOE_OP_FWD_MXFP4, 64, 2, 4, 256, 512)
     assert need > 0 and _fwd(wsb=need - 1) == WORKSPACE and _fwd(ws=None) == WORKSPACE and _fwd(ws=M) == WORKSPACE
@@ -105,11 +109,24 @@ def test_scale_bytes_of_the_python_layer(g, r, k):
     assert mxfp4._scale_bytes(g, r, k) == lib.moe_mx_scale_bytes(g, r, k)
 
 
+def test_tile_scales_call():
+    f = lib._lib.moe_mxfp4_tile_scales
+    assert f(P, 4, 64, 64, 2, 1, None, None) == INVALID and f(None, 4, 64, 64, 2, 0, P, None) == INVALID
+    assert f(P, 4, 64, 64, 1, 1, P, None) == INVALID and f(P, 4, 64, 48, 2, 1, P, None) == INVALID
+    assert f(P, 4, 64, 64, 2, 2, P, None) == INVALID and f(P, -1, 64, 64, 2, 1, P, None) == INVALID
+    assert f(P, 4, 64, 64, 2, 1, M, None) == INVALID
+    assert f(None, 0, 64, 64, 2, 1, None, None) == 0
+    size = lib.moe_mxfp4_tiled_scale_bytes
+    assert size(2, 97, 257 * 32, 1) == 2 * 2 * 33 * 1536 and size(3, 192, 256, 0) == 3 * 1536
+    assert size(3, 193, 288, 0) == 3 * 2 * 2 * 1536 and size(1, 64, 33, 0) == -1 and size(1, 64, 32, 5) == -1
+
+
 def test_half_the_bytes_of_the_mxfp8_recipe():
     """Codes of 4 bits: a layer's MXFP4 weights take half of its MXFP8 ones."""
     E, H, I = 8, 4096, 14336
     q8, sf = 3 * E * H * I, lib.moe_mx_scale_bytes(2 * E, I, H) + lib.moe_mx_scale_bytes(E, H, I)
-    assert (q8 // 2 + sf) / (q8 + sf) < 0.52
+    sf4 = lib.moe_mxfp4_tiled_scale_bytes(E, I, H, 1) + lib.moe_mxfp4_tiled_scale_bytes(E, H, I, 0)
+    assert (q8 // 2 + sf4) / (q8 + sf) < 0.52
 
 
 def test_python_layer_refuses_before_any_call():
