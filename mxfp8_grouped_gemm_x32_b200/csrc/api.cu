@@ -64,10 +64,10 @@ inline bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) ==
 inline bool al_elem(const void* p, int32_t dtype) {
   return (reinterpret_cast<uintptr_t>(p) & (dtype == MOE_DTYPE_BF16 ? 1u : 3u)) == 0;
 }
-// 32-bit row and unit numbers in the MXFP4 quantisation kernels
+// 32-bit row and block numbers in the MXFP4 quantisation kernels
 inline bool mxfp4_size_ok(int64_t groups, int64_t rows, int64_t cols) {
-  const int64_t lim = MXFP4_MAX_UNITS - (int64_t(1) << 24);  // and a grid's stride above
-  return rows < lim && cols / 8 < lim && rows * (cols / 8) < lim && groups * (rows * (cols / 8)) < lim;
+  const int64_t lim = MXFP4_MAX_BLOCKS, kb = cols / 32;
+  return rows < lim && kb < lim && rows * kb < lim && groups * (rows * kb) < lim;
 }
 inline int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
@@ -1122,7 +1122,7 @@ moe_status_t moe_grouped_mlp_fwd_mxfp4(const uint8_t* w1q, int64_t ld1, const ui
       (T > 0 && (!x || !out || !slot_to_row)))
     return MOE_ERR_INVALID;
   if (!layer_dims_ok(T, H, I, E, k)) return MOE_ERR_UNSUPPORTED;
-  if (int64_t(T) * (H / 8) >= MXFP4_MAX_UNITS - (int64_t(1) << 24)) return MOE_ERR_UNSUPPORTED;
+  if (int64_t(T) * (H / 32) >= MXFP4_MAX_BLOCKS) return MOE_ERR_UNSUPPORTED;
   if (rows_cap < moe_padded_rows(T, k, E) || rows_cap % 128) return MOE_ERR_INVALID;
   for (const void* p : {(const void*)w1q, (const void*)w1sf, (const void*)w2q, (const void*)w2sf, x,
                         (const void*)out})

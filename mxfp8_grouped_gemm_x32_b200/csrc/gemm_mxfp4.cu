@@ -16,8 +16,8 @@
 //                 (tcgen05.st); warp w writes lanes 32w.. of every column, so each
 //                 of the four reads all scales of the stage
 //   warps 4..11   epilogue: two groups of four, each with an accumulator
-//   warp 12       TMA producer (A, B boxes with 128-byte swizzle), 4-stage ring
-//   warp 13       the same for the scales (bulk copies), 8-stage ring
+//   warp 12       TMA producer (A, B boxes with 128-byte swizzle), ring of 4 or 5
+//   warp 13       the same for the scales (bulk copies), ring of 6 or 8
 //   warp 14       TMEM owner and MMA issuer; a stage is ready when its copies have
 //                 landed and the four scale warps have stored its scales
 // What bounds it, measured on the Mixtral gate_up shape (3.85 TFLOP) with parts
@@ -110,9 +110,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xFFFFFFFFu, ok);
 }
 
+template <int EPI>
 struct Cfg4 {
+  static constexpr bool ROWS = EPI == EPI4_F24_ROWS;
   static constexpr int TM = 128, TN = 192, BKB = 128;  // tile rows, columns, bytes of K
-  static constexpr int STAGES = 4;
+  // the rows' staging buffers take the place of a stage and two of the scales' ring
+  static constexpr int STAGES = ROWS ? 4 : 5;
   static constexpr int SF_WARPS = 4, EPI_WARPS = 8, PRODUCER = SF_WARPS + EPI_WARPS, SF_PRODUCER = PRODUCER + 1, ISSUER = PRODUCER + 2;
   static constexpr int THREADS = 32 * (ISSUER + 1);
   // TMEM columns: two accumulators, then per stage the scales of A (two atoms
@@ -123,11 +126,12 @@ struct Cfg4 {
   // scales of a K tile: two 512-byte atoms of A, 48 bytes a lane of B.  Their
   // ring is deeper than the operands': a K tile's scales take one hop more
   // (through the scale warps) to the MMA
-  static constexpr int SMEM_SF = 1024 + MXFP4_TILE_SF, SF_RING = 8;
+  static constexpr int SMEM_SF = 1024 + MXFP4_TILE_SF, SF_RING = ROWS ? 6 : 8;
   static constexpr int OFF_A = 0, OFF_B = OFF_A + STAGES * SMEM_A, OFF_SF = OFF_B + STAGES * SMEM_B;
   static constexpr int OFF_STAGE = OFF_SF + SF_RING * SMEM_SF;
-  // per epilogue warp: 32 rows of 32 packed f24 values, the source of its TMA stores
-  static constexpr int STAGE_WARP_BYTES = 32 * 96;
+  // per epilogue warp: 32 rows of 32 packed f24 values, twice, the sources of its
+  // TMA stores
+  static constexpr int STAGE_WARP_BYTES = ROWS ? 2 * 32 * 96 : 0;
   static constexpr int OFF_BAR = OFF_STAGE + EPI_WARPS * STAGE_WARP_BYTES;
   static constexpr int NUM_BARS = 3 * STAGES + 2 * SF_RING + 5;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8, OFF_GO = OFF_MISC + 16;
@@ -136,7 +140,7 @@ struct Cfg4 {
 };
 // columns of D per tile: EPI4_SWIGLU 96 of h (96 gate and 96 up), else all
 template <int EPI>
-constexpr int TILE_COLS = EPI == EPI4_SWIGLU ? Cfg4::TN / 2 : Cfg4::TN;
+constexpr int TILE_COLS = EPI == EPI4_SWIGLU ? Cfg4<EPI>::TN / 2 : Cfg4<EPI>::TN;
 
 struct Tile4 {
   int e, m0, n0, row_end;
@@ -163,14 +167,15 @@ __device__ __forceinline__ Tile4 decode_tile4(const Gemm4Args& a, const int* go,
 }
 
 // TMA store of a 32-row, 96-byte box from shared memory, as one bulk group; waits
-// until the thread's groups have read their sources, or are complete.
+// until all of the thread's groups but the last have read their sources, or until
+// all are complete.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int c0, int c1) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\tcp.async.bulk.commit_group;" ::"l"(
                    map),
                "r"(smem_u32(src)), "r"(c0), "r"(c1)
                : "memory");
 }
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // A producer's place in the ring.  The barrier of the stage after the current one
@@ -203,7 +208,7 @@ __device__ __forceinline__ void drain_copies(uint64_t* loaded, uint32_t issued) 
 // last read is followed by done(), which releases the accumulator.
 template <int EPI, typename Done>
 __device__ __forceinline__ void epilogue_tile4(const Gemm4Args& a, const CUtensorMap* tmY, const Tile4& ti, uint32_t tl,
-                                               int q, int lane, uint32_t* stage, Done done) {
+                                               int q, int lane, uint32_t* stage, uint32_t& turn, Done done) {
   const int N = a.N;
   if constexpr (EPI == EPI4_SWIGLU) {
     const int r = ti.m0 + 32 * q + lane;
@@ -257,24 +262,26 @@ __device__ __forceinline__ void epilogue_tile4(const Gemm4Args& a, const CUtenso
         const uint32_t u0 = v[4 * i], u1 = v[4 * i + 1], u2 = v[4 * i + 2], u3 = v[4 * i + 3];
         f24_pack4(u0, u1, u2, u3, v[3 * i], v[3 * i + 1], v[3 * i + 2]);
       }
-      if (lane == 0) bulk_wait_read();  // the buffer's last store has read it
+      if (lane == 0) bulk_wait_read1();  // the buffer's last store, the one before the last, has read it
       __syncwarp();
-      uint4* row = reinterpret_cast<uint4*>(stage + 24 * lane);
+      uint32_t* buf = stage + turn * (32 * 24);
+      turn ^= 1u;
+      uint4* row = reinterpret_cast<uint4*>(buf + 24 * lane);
 #pragma unroll
       for (int i = 0; i < 6; ++i) row[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) tma_store_2d(tmY, stage, (ti.n0 + 32 * c) * 3, ti.m0 + 32 * q);
+      if (lane == 0) tma_store_2d(tmY, buf, (ti.n0 + 32 * c) * 3, ti.m0 + 32 * q);
     }
   }
 }
 
 template <int EPI>
-__global__ void __launch_bounds__(Cfg4::THREADS, 1)
+__global__ void __launch_bounds__(Cfg4<EPI>::THREADS, 1)
     grouped_mxf4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
                              const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmY,
                              const Gemm4Args a) {
-  using C = Cfg4;
+  using C = Cfg4<EPI>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -371,12 +378,12 @@ __global__ void __launch_bounds__(Cfg4::THREADS, 1)
     const int q = warp & 3;                     // TMEM sub-partition this warp may read
     const int buf = (warp - C::SF_WARPS) >> 2;  // its accumulator: the CTA's even or odd tiles
     uint32_t* stage = reinterpret_cast<uint32_t*>(smem + C::OFF_STAGE + (warp - C::SF_WARPS) * C::STAGE_WARP_BYTES);
-    uint32_t use = 0;
+    uint32_t use = 0, turn = 0;  // turn: the staging buffer of the warp's next store
     for (int t = blockIdx.x + buf * gridDim.x; t < ntiles; t += 2 * gridDim.x) {
       const Tile4 ti = decode_tile4<EPI>(a, go, nt, t);
       if (!warp_wait(&acc_full[buf], use & 1u, abort_flag)) break;
       tc_fence_after();
-      epilogue_tile4<EPI>(a, &tmY, ti, tmem + (uint32_t(32 * q) << 16) + uint32_t(buf) * C::ACC_STRIDE, q, lane, stage, [&] {
+      epilogue_tile4<EPI>(a, &tmY, ti, tmem + (uint32_t(32 * q) << 16) + uint32_t(buf) * C::ACC_STRIDE, q, lane, stage, turn, [&] {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&acc_empty[buf]);
@@ -539,10 +546,10 @@ cudaError_t launch_epi4(const CUtensorMap& ma, const CUtensorMap& ma32, const CU
                         const Gemm4Args& a, int64_t tiles, cudaStream_t st) {
   static std::atomic<uint64_t> configured{0};
   auto kern = grouped_mxf4_gemm_kernel<EPI>;
-  cudaError_t e = ensure_smem_limit(kern, Cfg4::SMEM_LAUNCH, configured);
+  cudaError_t e = ensure_smem_limit(kern, Cfg4<EPI>::SMEM_LAUNCH, configured);
   if (e != cudaSuccess) return e;
   const int64_t sms = device_sm_count();
-  kern<<<unsigned(tiles < sms ? tiles : sms), Cfg4::THREADS, Cfg4::SMEM_LAUNCH, st>>>(ma, ma32, mb, my, a);
+  kern<<<unsigned(tiles < sms ? tiles : sms), Cfg4<EPI>::THREADS, Cfg4<EPI>::SMEM_LAUNCH, st>>>(ma, ma32, mb, my, a);
   count_launch();
   return cudaGetLastError();
 }
@@ -572,16 +579,16 @@ cudaError_t launch_grouped_gemm_mxfp4(int epi, const uint8_t* a_codes, int64_t r
   const int64_t row_tiles = groups + max_rows / 128;  // at most: every group ends inside a tile
   const int64_t inner = a.K / 2, pitch = mxfp4_pitch(a.K);
   CUtensorMap ma, ma32, mb, my;
-  cudaError_t e = make_map4(&ma, a_codes, inner, rows_cap, 0, pitch, 128, Cfg4::TM);
+  cudaError_t e = make_map4(&ma, a_codes, inner, rows_cap, 0, pitch, 128, Cfg4<EPI4_SWIGLU>::TM);
   if (e == cudaSuccess) e = make_map4(&ma32, a_codes, inner, rows_cap, 0, pitch, 128, 32);
   if (e != cudaSuccess) return e;
   if (epi == EPI4_SWIGLU) {
-    e = make_map4(&mb, b_codes, inner, a.N, 2 * int64_t(a.E), b_pitch, 128, Cfg4::TN / 2);
+    e = make_map4(&mb, b_codes, inner, a.N, 2 * int64_t(a.E), b_pitch, 128, TILE_COLS<EPI4_SWIGLU>);
     if (e != cudaSuccess) return e;
     return launch_epi4<EPI4_SWIGLU>(ma, ma32, mb, mb, a, row_tiles * cdiv(a.N, TILE_COLS<EPI4_SWIGLU>), st);
   }
   if (epi != EPI4_F24_ROWS) return cudaErrorInvalidValue;
-  e = make_map4(&mb, b_codes, inner, a.N, a.E, b_pitch, 128, Cfg4::TN);
+  e = make_map4(&mb, b_codes, inner, a.N, a.E, b_pitch, 128, TILE_COLS<EPI4_F24_ROWS>);
   if (e == cudaSuccess) e = make_map4(&my, a.out, 3 * int64_t(a.N), rows_cap, 0, 3 * int64_t(a.N), 96, 32);
   if (e != cudaSuccess) return e;
   return launch_epi4<EPI4_F24_ROWS>(ma, ma32, mb, my, a, row_tiles * cdiv(a.N, TILE_COLS<EPI4_F24_ROWS>), st);

@@ -46,10 +46,11 @@ struct Mxfp4Args {
   uint8_t* sf;
   int32_t groups;
   int64_t rows, K, ldq;
-  FastDiv units_div, rows_div;  // K / 8 and rows (set by the launcher)
+  FastDiv blocks_div, rows_div;  // K / 32 and rows (set by the launcher)
 };
-// units of 8 values have to be fewer than this (32-bit indices)
-constexpr int64_t MXFP4_MAX_UNITS = int64_t(1) << 31;
+// blocks of 32 values have to be fewer than this (their numbers and a grid's
+// stride fit 31 bits)
+constexpr int64_t MXFP4_MAX_BLOCKS = (int64_t(1) << 29) - (int64_t(1) << 22);
 cudaError_t launch_mxfp4_quant(Mxfp4Args a, bool bf16, cudaStream_t st);
 cudaError_t launch_mxfp4_dequant(Mxfp4Args a, bool bf16, cudaStream_t st);
 
@@ -62,7 +63,7 @@ struct Mxfp4ScatterArgs {
   const int32_t* slot_to_row;
   uint8_t* q;   // [rows_cap][H/2], mxfp4_pitch(H) bytes a row
   uint8_t* sf;  // blocked (1, rows_cap, H)
-  FastDiv units_div;  // H / 8 (set by the launcher)
+  FastDiv blocks_div;  // H / 32 (set by the launcher)
 };
 cudaError_t launch_mxfp4_quant_scatter(Mxfp4ScatterArgs a, cudaStream_t st);
 
