@@ -110,6 +110,46 @@ __host__ __device__ __forceinline__ int64_t sf_offset(int64_t g, int64_t r, int6
 
 __host__ __device__ __forceinline__ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// ---- dependent launches ------------------------------------------------------
+// A kernel launched with launch_dependent may start while the one before it in the
+// stream still runs, so its launch and set-up overlap that kernel's end.  Every
+// thread of it calls dependency_wait() before it touches global memory: that
+// returns once all earlier kernels are complete and their writes visible.
+// (Kernels that exit without it would let later ones overtake the earlier.)
+// release_dependents() lets the next kernel start; both do nothing in a kernel
+// launched in the ordinary way.  Pointers whose data is read with non-coherent
+// loads (__ldg, const __restrict__) are given to dependency_wait, behind which
+// they count as new: the compiler takes such data for constant and might
+// otherwise load it before the wait.
+template <typename P>
+__device__ __forceinline__ void renew(P& p) {
+  asm volatile("" : "+l"(p)::"memory");
+}
+template <typename... P>
+__device__ __forceinline__ void dependency_wait(P&... p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  (renew(p), ...);
+}
+__device__ __forceinline__ void release_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... Params, typename... Args>
+inline cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
+                                    cudaStream_t st, Args... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+  count_launch();
+  return e;
+}
+
 // ---- per-device host-side setup --------------------------------------------
 // SM count of the current device (cached per device; 148 if unknown).
 inline int device_sm_count() {

@@ -324,6 +324,8 @@ __global__ void __launch_bounds__(Cfg4<EPI>::THREADS, 1)
     tmem_alloc(tmem_slot, C::COLS);
     tmem_relinquish();
   }
+  release_dependents();
+  dependency_wait();  // the set-up above overlaps the kernel before this one
   for (int i = threadIdx.x; i <= a.E; i += C::THREADS) go[i] = a.group_offsets[i];
   tc_fence_before();
   __syncthreads();
@@ -549,9 +551,8 @@ cudaError_t launch_epi4(const CUtensorMap& ma, const CUtensorMap& ma32, const CU
   cudaError_t e = ensure_smem_limit(kern, Cfg4<EPI>::SMEM_LAUNCH, configured);
   if (e != cudaSuccess) return e;
   const int64_t sms = device_sm_count();
-  kern<<<unsigned(tiles < sms ? tiles : sms), Cfg4<EPI>::THREADS, Cfg4<EPI>::SMEM_LAUNCH, st>>>(ma, ma32, mb, my, a);
-  count_launch();
-  return cudaGetLastError();
+  return launch_dependent(kern, unsigned(tiles < sms ? tiles : sms), Cfg4<EPI>::THREADS, Cfg4<EPI>::SMEM_LAUNCH, st, ma,
+                          ma32, mb, my, a);
 }
 
 // Bytes [rows][inner] (of one of `groups` matrices), rows `pitch` bytes apart, in

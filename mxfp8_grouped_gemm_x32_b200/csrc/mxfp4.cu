@@ -176,19 +176,23 @@ __global__ void __launch_bounds__(Q4_THREADS) mxfp4_dequant_kernel(const Mxfp4Ar
 
 template <bool WORDS>
 __global__ void __launch_bounds__(Q4_THREADS) mxfp4_quant_scatter_kernel(const Mxfp4ScatterArgs a) {
+  const uint8_t* src = a.src;
+  const int32_t* slot_to_row = a.slot_to_row;
+  release_dependents();
+  dependency_wait(src, slot_to_row);
   const uint32_t KB = a.blocks_div.d, KT = (KB + 3) / 4;
   const uint32_t n = uint32_t(a.T) * KB;  // < 2^29 (checked by the launcher)
   const int64_t pitch = mxfp4_pitch(a.H);
   const uint32_t stride = gridDim.x * Q4_THREADS;
-  const bool wide = (reinterpret_cast<uintptr_t>(a.src) & 31u) == 0;
+  const bool wide = (reinterpret_cast<uintptr_t>(src) & 31u) == 0;
   for (uint32_t i0 = blockIdx.x * Q4_THREADS + (threadIdx.x & ~31u); i0 < n; i0 += stride) {
     const uint32_t i = i0 + (threadIdx.x & 31);
     const bool in = i < n;
     const uint32_t b = in ? i : n - 1;
     const uint32_t t = fastdiv(b, a.blocks_div), kb = b - t * KB;
-    const int32_t* rows = a.slot_to_row + int64_t(t) * a.k;
+    const int32_t* rows = slot_to_row + int64_t(t) * a.k;
     float f[32];
-    load32<true>(a.src, b, wide, f);
+    load32<true>(src, b, wide, f);
     const int32_t first = __ldg(rows);
     uint32_t sb;
     const uint4 w = encode32(f, sb);
@@ -257,10 +261,8 @@ cudaError_t launch_mxfp4_quant_scatter(Mxfp4ScatterArgs a, cudaStream_t st) {
   if (blocks == 0) return cudaSuccess;
   if (blocks >= MXFP4_MAX_BLOCKS) return cudaErrorInvalidValue;
   a.blocks_div = make_fastdiv(uint32_t(a.H / 32));
-  (a.H % 128 == 0 ? mxfp4_quant_scatter_kernel<true> : mxfp4_quant_scatter_kernel<false>)<<<q4_blocks(blocks, 16), Q4_THREADS,
-                                                                                       0, st>>>(a);
-  count_launch();
-  return cudaGetLastError();
+  return launch_dependent(a.H % 128 == 0 ? mxfp4_quant_scatter_kernel<true> : mxfp4_quant_scatter_kernel<false>,
+                          q4_blocks(blocks, 16), Q4_THREADS, 0, st, a);
 }
 
 }  // namespace moe

@@ -15,10 +15,18 @@ constexpr int PB = PERM_BLOCK;
 
 __device__ __forceinline__ bool id_ok(int32_t e, int32_t E) { return e >= 0 && e < E; }
 
-// Pass 1: per-block expert histogram.
+// Pass 1: per-block expert histogram; the row maps' empty values (-1 and 0) for
+// all rows along the way.
 __global__ void __launch_bounds__(PB) perm_hist_kernel(const int32_t* __restrict__ idx, int64_t R,
-                                                       int32_t E, int32_t* __restrict__ hist) {
+                                                       int32_t E, int32_t* __restrict__ hist, int64_t rows_cap,
+                                                       int32_t* __restrict__ row_to_slot, float* __restrict__ prob_perm) {
+  release_dependents();
+  dependency_wait(idx);
   extern __shared__ int cnt[];
+  for (int64_t i = int64_t(blockIdx.x) * PB + threadIdx.x; i < rows_cap; i += int64_t(gridDim.x) * PB) {
+    row_to_slot[i] = -1;
+    prob_perm[i] = 0.0f;
+  }
   for (int i = threadIdx.x; i < E; i += PB) cnt[i] = 0;
   __syncthreads();
   const int64_t s = int64_t(blockIdx.x) * PB + threadIdx.x;
@@ -35,41 +43,72 @@ __global__ void __launch_bounds__(PB) perm_hist_kernel(const int32_t* __restrict
 
 // Pass 2 (one CTA): split_sizes, 128-aligned group offsets, and the first
 // row of every (block, expert) pair relative to its group's start, in place
-// in `hist` (the scatter adds the group offset).  Each expert's column of
-// block counts is read eight blocks at a time so that the loads overlap.
-__global__ void __launch_bounds__(MOE_MAX_EXPERTS) perm_scan_kernel(int32_t* __restrict__ hist,
-                                                                    int32_t nblocks, int32_t E,
-                                                                    int32_t* __restrict__ split,
-                                                                    int32_t* __restrict__ offs) {
-  __shared__ int32_t padded[MOE_MAX_EXPERTS + 1];
-  const int e = threadIdx.x;
-  int32_t total = 0;
-  if (e < E) {
-    for (int b0 = 0; b0 < nblocks; b0 += 8) {
+// in `hist` (the scatter adds the group offset).  PERM_SEGMENTS threads share
+// an expert's column of block counts, a run of blocks each, read eight at a
+// time so that the loads overlap: once for the runs' sums, once more for the
+// prefixes.
+constexpr int PERM_SEGMENTS = 4;
+__global__ void __launch_bounds__(MOE_MAX_EXPERTS* PERM_SEGMENTS) perm_scan_kernel(int32_t* __restrict__ hist,
+                                                                                  int32_t nblocks, int32_t E,
+                                                                                  int32_t* __restrict__ split,
+                                                                                  int32_t* __restrict__ offs) {
+  release_dependents();
+  dependency_wait();
+  __shared__ int32_t run_sum[PERM_SEGMENTS][MOE_MAX_EXPERTS];
+  __shared__ int32_t wsum[MOE_MAX_EXPERTS / 32];
+  const int e = threadIdx.x % MOE_MAX_EXPERTS, seg = threadIdx.x / MOE_MAX_EXPERTS, lane = threadIdx.x & 31;
+  const int per = (nblocks + PERM_SEGMENTS - 1) / PERM_SEGMENTS;
+  const int first = seg * per, last = min(nblocks, first + per);
+  int32_t sum = 0;
+  if (e < E)
+    for (int b0 = first; b0 < last; b0 += 8) {
       int32_t c[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) c[i] = b0 + i < nblocks ? hist[int64_t(b0 + i) * E + e] : 0;
+      for (int i = 0; i < 8; ++i) c[i] = b0 + i < last ? hist[int64_t(b0 + i) * E + e] : 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += c[i];
+    }
+  run_sum[seg][e] = sum;
+  __syncthreads();
+  int32_t before = 0, total = 0;
+#pragma unroll
+  for (int s = 0; s < PERM_SEGMENTS; ++s) {
+    if (s < seg) before += run_sum[s][e];
+    total += run_sum[s][e];
+  }
+  if (e < E)
+    for (int b0 = first; b0 < last; b0 += 8) {
+      int32_t c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = b0 + i < last ? hist[int64_t(b0 + i) * E + e] : 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (b0 + i < nblocks) hist[int64_t(b0 + i) * E + e] = total;
-        total += c[i];
+        if (b0 + i < last) hist[int64_t(b0 + i) * E + e] = before;
+        before += c[i];
       }
     }
-    split[e] = total;
-  }
-  padded[e] = e < E ? (total + 127) / 128 * 128 : 0;
-  __syncthreads();
-  if (e == 0) {
-    int32_t run = 0;
-    for (int i = 0; i < E; ++i) {
-      const int32_t p = padded[i];
-      padded[i] = run;
-      run += p;
+  // group offsets: exclusive scan of the groups' padded rows (segment 0's warps)
+  int32_t padded = 0, incl = 0;
+  if (seg == 0) {
+    if (e < E) {
+      split[e] = total;
+      padded = (total + 127) / 128 * 128;
     }
-    offs[E] = run;
+    incl = padded;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    if (lane == 31) wsum[threadIdx.x >> 5] = incl;
   }
   __syncthreads();
-  if (e < E) offs[e] = padded[e];
+  if (seg == 0 && e < E) {
+    int32_t base = 0;
+    for (int w = 0; w < int(threadIdx.x >> 5); ++w) base += wsum[w];
+    offs[e] = base + incl - padded;
+    if (e == E - 1) offs[E] = base + incl;
+  }
 }
 
 // Pass 3: stable rank of every slot inside its block (warp match + per-warp
@@ -82,6 +121,8 @@ __global__ void __launch_bounds__(PB) perm_scatter_kernel(const int32_t* __restr
                                                           int32_t* __restrict__ slot_to_row,
                                                           int32_t* __restrict__ row_to_slot,
                                                           float* __restrict__ prob_perm) {
+  release_dependents();
+  dependency_wait(idx, prob, base, offs);
   extern __shared__ int wcnt[];  // [32 warps][E]
   for (int i = threadIdx.x; i < 32 * E; i += PB) wcnt[i] = 0;
   __syncthreads();
@@ -120,6 +161,8 @@ __global__ void __launch_bounds__(PB) perm_small_kernel(const int32_t* __restric
                                                         int32_t* __restrict__ offs, int32_t* __restrict__ slot_to_row,
                                                         int32_t* __restrict__ row_to_slot,
                                                         float* __restrict__ prob_perm) {
+  release_dependents();
+  dependency_wait(idx, prob);
   extern __shared__ int wcnt[];  // [32 warps][E]: counts, then first ranks; then [E + 1] group offsets
   __shared__ int wsum[MOE_MAX_EXPERTS / 32];
   int* goff = wcnt + 32 * E;
@@ -194,6 +237,8 @@ __global__ void __launch_bounds__(PB) perm_small_kernel(const int32_t* __restric
 template <int FMT>
 __global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ yv, const int32_t* __restrict__ slot_to_row,
                                                       int64_t T, int32_t k, int64_t H8, uint4* __restrict__ out) {
+  release_dependents();
+  dependency_wait(yv, slot_to_row);
   const int64_t n = T * H8;
   for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < n;
        i += int64_t(gridDim.x) * blockDim.x) {
@@ -237,14 +282,12 @@ cudaError_t launch_permute_scan_scatter(const int32_t* idx, const float* prob, i
                                         float* prob_perm, void* ws, cudaStream_t st) {
   const int32_t nb = int32_t(cdiv(R, PB));
   int32_t* hist = static_cast<int32_t*>(ws);
-  perm_scan_kernel<<<1, MOE_MAX_EXPERTS, 0, st>>>(hist, nb, E, split, offs);
-  count_launch();
-  if (nb > 0) {
-    perm_scatter_kernel<<<nb, PB, 32 * E * sizeof(int), st>>>(idx, prob, R, E, hist, offs, slot_to_row,
-                                                               row_to_slot, prob_perm);
-    count_launch();
-  }
-  return cudaGetLastError();
+  cudaError_t err =
+      launch_dependent(perm_scan_kernel, 1, MOE_MAX_EXPERTS * PERM_SEGMENTS, 0, st, hist, nb, E, split, offs);
+  if (err == cudaSuccess && nb > 0)
+    err = launch_dependent(perm_scatter_kernel, unsigned(nb), PB, 32 * E * sizeof(int), st, idx, prob, R, E, hist, offs,
+                           slot_to_row, row_to_slot, prob_perm);
+  return err;
 }
 
 cudaError_t launch_permute_index(const int32_t* idx, const float* prob, int64_t R, int32_t E,
@@ -252,21 +295,14 @@ cudaError_t launch_permute_index(const int32_t* idx, const float* prob, int64_t 
                                  int32_t* row_to_slot, int32_t* slot_to_row, float* prob_perm,
                                  void* ws, cudaStream_t st) {
   if (R > 0 && R <= PB) {
-    perm_small_kernel<<<1, PB, 33 * E * sizeof(int), st>>>(idx, prob, int32_t(R), E, rows_cap, split, offs,
-                                                           slot_to_row, row_to_slot, prob_perm);
-    count_launch();
-    return cudaGetLastError();
+    return launch_dependent(perm_small_kernel, 1, PB, 33 * E * sizeof(int), st, idx, prob, int32_t(R), E, rows_cap, split,
+                            offs, slot_to_row, row_to_slot, prob_perm);
   }
-  cudaError_t err = cudaMemsetAsync(row_to_slot, 0xFF, size_t(rows_cap) * 4, st);
-  if (err != cudaSuccess) return err;
-  err = cudaMemsetAsync(prob_perm, 0, size_t(rows_cap) * 4, st);
-  if (err != cudaSuccess) return err;
+  // (an empty batch too: one block, no slots)
   const int32_t nb = int32_t(cdiv(R, PB));
-  int32_t* hist = static_cast<int32_t*>(ws);
-  if (nb > 0) {
-    perm_hist_kernel<<<nb, PB, E * sizeof(int), st>>>(idx, R, E, hist);
-    count_launch();
-  }
+  const cudaError_t err = launch_dependent(perm_hist_kernel, unsigned(nb < 1 ? 1 : nb), PB, E * sizeof(int), st, idx, R, E,
+                                           static_cast<int32_t*>(ws), rows_cap, row_to_slot, prob_perm);
+  if (err != cudaSuccess) return err;
   return launch_permute_scan_scatter(idx, prob, R, E, split, offs, row_to_slot, slot_to_row, prob_perm, ws, st);
 }
 
@@ -277,14 +313,9 @@ cudaError_t launch_combine(const void* y, int fmt, const int32_t* slot_to_row, i
   int64_t blocks = cdiv(n, 256);
   if (blocks > 148 * 32) blocks = 148 * 32;
   uint4* o = static_cast<uint4*>(out);
-  if (fmt == COMBINE_F32)
-    combine_kernel<COMBINE_F32><<<unsigned(blocks), 256, 0, st>>>(y, slot_to_row, T, k, H / 8, o);
-  else if (fmt == COMBINE_F24)
-    combine_kernel<COMBINE_F24><<<unsigned(blocks), 256, 0, st>>>(y, slot_to_row, T, k, H / 8, o);
-  else
-    combine_kernel<COMBINE_BF16><<<unsigned(blocks), 256, 0, st>>>(y, slot_to_row, T, k, H / 8, o);
-  count_launch();
-  return cudaGetLastError();
+  auto kern = fmt == COMBINE_F32 ? combine_kernel<COMBINE_F32>
+                                 : (fmt == COMBINE_F24 ? combine_kernel<COMBINE_F24> : combine_kernel<COMBINE_BF16>);
+  return launch_dependent(kern, unsigned(blocks), 256, 0, st, y, slot_to_row, T, k, H / 8, o);
 }
 
 }  // namespace moe
