@@ -31,7 +31,14 @@ namespace {
 
 constexpr int RL_THREADS = 256;
 constexpr int RL_WARPS = RL_THREADS / 32;
-constexpr int RL_BLOCKS_PER_SM = 3;
+// Wide rows (groups of 16 or 32 lanes): four blocks per SM, a token's logits loaded
+// when they are needed.  Narrow ones: three, with the next token's logits on their
+// way -- more kept experts per lane need more registers (gradient of 262144 x 256:
+// 109 against 125 us, x 32: 45 against 41).
+template <int G>
+constexpr bool RL_WIDE = G >= 16;
+template <int G>
+constexpr int RL_BLOCKS_PER_SM = RL_WIDE<G> ? 4 : 3;
 // most experts that a token of a group of G lanes keeps
 template <int G>
 constexpr int KEPT_MAX = G < 4 ? 8 * G : 32;
@@ -206,8 +213,9 @@ struct LossPartials {
 // and id to shared memory; equal values go to the lowest lane, whose experts
 // have the lower ids.
 template <bool BF16, int G>
-__global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM)
+__global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM<G>)
     router_loss_kernel(const RouterLossArgs a, const LossPartials part, const bool vec) {
+  constexpr bool AHEAD = !RL_WIDE<G>;
   constexpr int GROUPS = 32 / G;               // tokens per warp
   constexpr int KL = (KEPT_MAX<G> + G - 1) / G;  // kept experts per lane
   __shared__ float2 list[RL_WARPS * GROUPS][KEPT_MAX<G> + 1];  // (value, id as bits) of a token's kept experts
@@ -242,16 +250,20 @@ __global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM)
   // token works on the last one and keeps nothing
   const int step = int(gridDim.x) * per;
   int t0 = int(blockIdx.x) * per + warp * GROUPS;
-  float next[8];  // the logits of the token after this one are on their way
-  if (t0 < a.T) load_row8<BF16>(a.logits, min(t0 + sub, a.T - 1), E, g, vec, next);
+  float next[8];  // AHEAD: the logits of the token after this one are on their way
+  if (AHEAD && t0 < a.T) load_row8<BF16>(a.logits, min(t0 + sub, a.T - 1), E, g, vec, next);
   for (; t0 < a.T; t0 += step) {
     const bool in = t0 + sub < a.T;
     const int t = in ? t0 + sub : a.T - 1;
     const bool live = in && (!a.mask || a.mask[t] != 0);
     float v[8];
+    if constexpr (AHEAD) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = next[i];
-    if (t0 + step < a.T) load_row8<BF16>(a.logits, min(t0 + step + sub, a.T - 1), E, g, vec, next);
+      for (int i = 0; i < 8; ++i) v[i] = next[i];
+      if (t0 + step < a.T) load_row8<BF16>(a.logits, min(t0 + step + sub, a.T - 1), E, g, vec, next);
+    } else {
+      load_row8<BF16>(a.logits, t, E, g, vec, v);
+    }
     // a NaN among the lane's logits makes this sum NaN (and so may infinities)
     bool nan = false;
     const float probe = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
@@ -484,7 +496,9 @@ __global__ void __cluster_dims__(RF_CLUSTER, 1, 1) __launch_bounds__(RF_THREADS)
 // scattered to a zeroed row of shared memory, from which every lane adds its
 // eight; only where a token lists an expert twice are they added one by one.
 template <bool BF16, int G>
-__global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM) router_bwd_kernel(const RouterBwdArgs a, const bool vec) {
+__global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM<G>)
+    router_bwd_kernel(const RouterBwdArgs a, const bool vec) {
+  constexpr bool AHEAD = !RL_WIDE<G>;
   constexpr int GROUPS = 32 / G;
   constexpr int KL = (KEPT_MAX<G> + G - 1) / G;  // kept experts per lane
   __shared__ float share[8 * G];                      // f_e
@@ -511,7 +525,7 @@ __global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM) router_bwd_kerne
   bool live_next;
   auto fetch = [&](int t0) {
     const int t = min(t0 + sub, a.T - 1);
-    load_row8<BF16>(a.logits, t, E, g, vec, next);
+    if constexpr (AHEAD) load_row8<BF16>(a.logits, t, E, g, vec, next);
     next_lse = a.lse[t];
     live_next = t0 + sub < a.T && (!a.mask || a.mask[t] != 0);
     if (a.dprob) {
@@ -537,8 +551,12 @@ __global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM) router_bwd_kerne
     const float lse = next_lse;
     float d[8], p[KL], dp[KL];
     int32_t id[KL];
+    if constexpr (AHEAD) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) d[i] = next[i];
+      for (int i = 0; i < 8; ++i) d[i] = next[i];
+    } else {
+      load_row8<BF16>(a.logits, min(t, a.T - 1), E, g, vec, d);
+    }
 #pragma unroll
     for (int j = 0; j < KL; ++j) {
       p[j] = p_next[j];
@@ -627,9 +645,11 @@ int32_t group_width(int32_t E) {
   return g;
 }
 
-unsigned loss_blocks(int32_t T, int32_t E, int per_sm) {
-  const int64_t per = int64_t(RL_WARPS) * (32 / group_width(E));
-  const int64_t want = cdiv(int64_t(T), per), cap = int64_t(device_sm_count()) * per_sm;
+unsigned loss_blocks(int32_t T, int32_t E) {
+  const int32_t g = group_width(E);
+  const int64_t per = int64_t(RL_WARPS) * (32 / g);
+  const int64_t want = cdiv(int64_t(T), per);
+  const int64_t cap = int64_t(device_sm_count()) * (g >= 16 ? RL_BLOCKS_PER_SM<16> : RL_BLOCKS_PER_SM<1>);
   return unsigned(want < cap ? want : cap);
 }
 
@@ -643,12 +663,12 @@ bool rows_vectorised(const void* p, const void* q, int32_t E) {
 int64_t router_loss_workspace_bytes(int32_t T, int32_t E) {
   (void)T;
   // the most blocks the first kernel is launched with on a device of 1024 SMs
-  const int64_t blocks = 1024 * RL_BLOCKS_PER_SM;
+  const int64_t blocks = 1024 * RL_BLOCKS_PER_SM<16>;
   return blocks * (int64_t(E) * 8 + 8);
 }
 
 cudaError_t launch_router_losses(const RouterLossArgs& a, bool bf16, void* ws, cudaStream_t st) {
-  const unsigned blocks = a.T > 0 ? loss_blocks(a.T, a.E, RL_BLOCKS_PER_SM) : 0;
+  const unsigned blocks = a.T > 0 ? loss_blocks(a.T, a.E) : 0;
   LossPartials part;
   part.sums = static_cast<float*>(ws);
   part.counts = reinterpret_cast<int32_t*>(part.sums + int64_t(blocks) * a.E);
@@ -673,7 +693,7 @@ cudaError_t launch_router_losses(const RouterLossArgs& a, bool bf16, void* ws, c
 
 cudaError_t launch_router_bwd(const RouterBwdArgs& a, bool bf16, cudaStream_t st) {
   if (a.T == 0) return cudaSuccess;
-  const unsigned blocks = loss_blocks(a.T, a.E, RL_BLOCKS_PER_SM);
+  const unsigned blocks = loss_blocks(a.T, a.E);
   const bool vec = rows_vectorised(a.logits, a.dlogits, a.E);
   count_launch();
   return by_group(a.E, [&](auto G) {
