@@ -205,6 +205,121 @@ struct LossPartials {
   int32_t* n;       // [blocks]
 };
 
+// Sum over the block in a fixed order, the same in every thread.
+template <int THREADS>
+__device__ __forceinline__ double block_sum(double x, double* buf) {
+  __syncthreads();
+  buf[threadIdx.x] = x;
+  __syncthreads();
+  for (int s = THREADS / 2; s >= 1; s >>= 1) {
+    if (int(threadIdx.x) < s) buf[threadIdx.x] += buf[threadIdx.x + s];
+    __syncthreads();
+  }
+  return buf[0];
+}
+
+__device__ __forceinline__ double ld_cluster_f64(const double* p, uint32_t rank) {
+  double x;
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(x) : "r"(smem_in_cta(p, rank)) : "memory");
+  return x;
+}
+
+template <int THREADS>
+struct FinishShared {
+  double buf[THREADS];
+  int32_t ibuf[THREADS];
+  double sums[MOE_MAX_EXPERTS], counts[MOE_MAX_EXPERTS];  // this block's
+  double z, n;
+};
+
+// The cluster's blocks add the rows of partial sums up, block c the rows c, c + 8,
+// ..., four loads in flight per thread; block 0 then adds the blocks' sums, in
+// order, and writes the results.  Sums in 64 bits (counts too, exactly): a few
+// hundred terms of any size, and no cost next to the loads.
+template <int THREADS>
+__device__ __forceinline__ void finish_losses(const RouterLossArgs& a, const LossPartials& part, int blocks,
+                                              FinishShared<THREADS>& sh) {
+  const int c = int(cluster_ctarank()), tid = threadIdx.x;
+  int width = 32;  // threads across the experts, a power of two; the others split the rows
+  while (width < a.E) width *= 2;
+  const int e = tid & (width - 1), slice = tid / width, slices = THREADS / width;
+  double s = 0.0;
+  int32_t cnt = 0;
+  if (e < a.E)
+    for (int b0 = c + RF_CLUSTER * slice; b0 < blocks; b0 += 4 * RF_CLUSTER * slices) {
+      float x[4];
+      int32_t y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int b = b0 + i * RF_CLUSTER * slices;
+        x[i] = b < blocks ? part.sums[int64_t(b) * a.E + e] : 0.0f;
+        y[i] = b < blocks ? part.counts[int64_t(b) * a.E + e] : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s += double(x[i]);
+        cnt += y[i];
+      }
+    }
+  double z = 0.0, n = 0.0;
+  for (int b = c + RF_CLUSTER * tid; b < blocks; b += RF_CLUSTER * THREADS) {
+    z += double(part.z[b]);
+    n += double(part.n[b]);  // exact: below 2^53
+  }
+  sh.buf[tid] = s;
+  sh.ibuf[tid] = cnt;
+  __syncthreads();
+  if (tid < a.E) {
+    s = 0.0;
+    cnt = 0;
+    for (int w = 0; w < slices; ++w) {
+      s += sh.buf[w * width + tid];
+      cnt += sh.ibuf[w * width + tid];
+    }
+    sh.sums[tid] = s;
+    sh.counts[tid] = double(cnt);
+  }
+  z = block_sum<THREADS>(z, sh.buf);
+  n = block_sum<THREADS>(n, sh.buf);
+  if (tid == 0) {
+    sh.z = z;
+    sh.n = n;
+  }
+  cluster_sync_all();
+  if (c == 0) {
+    double dot = 0.0;
+    if (tid < a.E) {
+      s = n = 0.0;
+#pragma unroll
+      for (int r = 0; r < RF_CLUSTER; ++r) {
+        s += ld_cluster_f64(&sh.sums[tid], uint32_t(r));
+        n += ld_cluster_f64(&sh.counts[tid], uint32_t(r));
+      }
+      a.prob_sums[tid] = float(s);
+      a.counts[tid] = int32_t(n);
+      dot = s * n;
+    }
+    dot = block_sum<THREADS>(dot, sh.buf);
+    if (tid == 0) {
+      z = n = 0.0;
+      for (int r = 0; r < RF_CLUSTER; ++r) {
+        z += ld_cluster_f64(&sh.z, uint32_t(r));
+        n += ld_cluster_f64(&sh.n, uint32_t(r));
+      }
+      *a.tokens = int32_t(n);
+      a.losses[0] = n > 0.0 ? float(double(a.E) * dot / (n * n * double(a.k))) : 0.0f;
+      a.losses[1] = n > 0.0 ? float(z / n) : 0.0f;
+    }
+  }
+  cluster_sync_all();  // no block leaves while its shared memory is read
+}
+
+__global__ void __cluster_dims__(RF_CLUSTER, 1, 1) __launch_bounds__(RF_THREADS)
+    router_loss_finish_kernel(const RouterLossArgs a, const LossPartials part, const int blocks) {
+  __shared__ FinishShared<RF_THREADS> sh;
+  finish_losses<RF_THREADS>(a, part, blocks, sh);
+}
+
 // Selection: k rounds of a maximum over the group's lanes, each of which offers
 // the best of its experts not yet kept.  A lane prepares its two best at once
 // and looks again only after both were kept, which for 256 experts and k = 8
@@ -212,7 +327,8 @@ struct LossPartials {
 // instead of a scan of eight values.  The lane that wins writes the kept value
 // and id to shared memory; equal values go to the lowest lane, whose experts
 // have the lower ids.
-template <bool BF16, int G>
+// ONE: a batch so small that a cluster of eight blocks does it all in one launch.
+template <bool BF16, int G, bool ONE>
 __global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM<G>)
     router_loss_kernel(const RouterLossArgs a, const LossPartials part, const bool vec) {
   constexpr bool AHEAD = !RL_WIDE<G>;
@@ -400,96 +516,11 @@ __global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM<G>)
     part.z[blockIdx.x] = z;
     part.n[blockIdx.x] = c;
   }
-}
-
-// Sum over the finishing block in a fixed order, the same in every thread.
-__device__ __forceinline__ double block_sum(double x, double* buf) {
-  __syncthreads();
-  buf[threadIdx.x] = x;
-  __syncthreads();
-  for (int s = RF_THREADS / 2; s >= 1; s >>= 1) {
-    if (int(threadIdx.x) < s) buf[threadIdx.x] += buf[threadIdx.x + s];
-    __syncthreads();
+  if constexpr (ONE) {
+    __shared__ FinishShared<RL_THREADS> sh;
+    cluster_sync_all();  // the blocks' partial sums, written to global memory, are there
+    finish_losses<RL_THREADS>(a, part, RF_CLUSTER, sh);
   }
-  return buf[0];
-}
-
-// One cluster adds the blocks' rows up: block c owns the experts 32 c .. 32 c +
-// 31, one per lane, its warps every 32nd row, four loads in flight each.
-// Sums in 64 bits: a few hundred terms of any size, and no cost next to the
-// loads.
-__global__ void __cluster_dims__(RF_CLUSTER, 1, 1) __launch_bounds__(RF_THREADS)
-    router_loss_finish_kernel(const RouterLossArgs a, const LossPartials part, const int blocks) {
-  __shared__ double buf[RF_THREADS];
-  __shared__ int32_t ibuf[RF_THREADS / 32][32];
-  __shared__ double mine;  // this block's part of sum_e counts_e sums_e
-  static_assert(32 * RF_CLUSTER >= MOE_MAX_EXPERTS, "an expert per lane of the cluster");
-  constexpr int W = RF_THREADS / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = int(cluster_ctarank());
-  const int e = 32 * c + lane;
-  double s = 0.0;
-  int32_t cnt = 0;
-  if (e < a.E)
-    for (int b0 = warp; b0 < blocks; b0 += 4 * W) {
-      float x[4];
-      int32_t y[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int b = b0 + i * W;
-        x[i] = b < blocks ? part.sums[int64_t(b) * a.E + e] : 0.0f;
-        y[i] = b < blocks ? part.counts[int64_t(b) * a.E + e] : 0;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s += double(x[i]);
-        cnt += y[i];
-      }
-    }
-  double z = 0.0, n = 0.0;
-  if (c == 0)
-    for (int b = threadIdx.x; b < blocks; b += RF_THREADS) {
-      z += double(part.z[b]);
-      n += double(part.n[b]);  // exact: below 2^53
-    }
-  buf[threadIdx.x] = s;
-  ibuf[warp][lane] = cnt;
-  __syncthreads();
-  if (warp == 0) {
-    double dot = 0.0;
-    if (e < a.E) {
-      s = 0.0;
-      cnt = 0;
-#pragma unroll 8
-      for (int w = 0; w < W; ++w) {
-        s += buf[32 * w + lane];
-        cnt += ibuf[w][lane];
-      }
-      a.prob_sums[e] = float(s);
-      a.counts[e] = cnt;
-      dot = s * double(cnt);
-    }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, off);
-    if (lane == 0) mine = dot;
-  }
-  if (c == 0) {
-    z = block_sum(z, buf);
-    n = block_sum(n, buf);
-  }
-  cluster_sync_all();
-  if (c == 0 && threadIdx.x == 0) {
-    double total = 0.0;
-    for (int r = 0; r < RF_CLUSTER; ++r) {
-      double other;
-      asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(other) : "r"(smem_in_cta(&mine, uint32_t(r))) : "memory");
-      total += other;
-    }
-    *a.tokens = int32_t(n);
-    a.losses[0] = n > 0.0 ? float(double(a.E) * total / (n * n * double(a.k))) : 0.0f;
-    a.losses[1] = n > 0.0 ? float(z / n) : 0.0f;
-  }
-  cluster_sync_all();  // no block leaves while its shared memory is read
 }
 
 // Gradient of the logits, on the same lanes.  The k kept logits' gradients are
@@ -668,24 +699,38 @@ int64_t router_loss_workspace_bytes(int32_t T, int32_t E) {
 }
 
 cudaError_t launch_router_losses(const RouterLossArgs& a, bool bf16, void* ws, cudaStream_t st) {
-  const unsigned blocks = a.T > 0 ? loss_blocks(a.T, a.E) : 0;
+  // One launch where eight blocks need at most two passes over the tokens (512 tokens
+  // of four experts: 8.4 us, two launches 10.4); more passes take longer than the
+  // second launch
+  const bool one = a.T <= 2 * RF_CLUSTER * RL_WARPS * (32 / group_width(a.E));
+  const unsigned blocks = one ? RF_CLUSTER : loss_blocks(a.T, a.E);
   LossPartials part;
   part.sums = static_cast<float*>(ws);
   part.counts = reinterpret_cast<int32_t*>(part.sums + int64_t(blocks) * a.E);
   part.z = reinterpret_cast<float*>(part.counts + int64_t(blocks) * a.E);
   part.n = reinterpret_cast<int32_t*>(part.z + blocks);
-  if (blocks > 0) {
-    const bool vec = rows_vectorised(a.logits, a.logits, a.E);
-    cudaError_t e = by_group(a.E, [&](auto G) {
-      if (bf16)
-        router_loss_kernel<true, decltype(G)::value><<<blocks, RL_THREADS, 0, st>>>(a, part, vec);
-      else
-        router_loss_kernel<false, decltype(G)::value><<<blocks, RL_THREADS, 0, st>>>(a, part, vec);
-      return cudaGetLastError();
-    });
-    if (e != cudaSuccess) return e;
-    count_launch();
-  }
+  const bool vec = rows_vectorised(a.logits, a.logits, a.E);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = RF_CLUSTER;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(RL_THREADS);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = one ? 1 : 0;
+  const cudaError_t e = by_group(a.E, [&](auto G) {
+    constexpr int W = decltype(G)::value;
+    if (one)
+      return cudaLaunchKernelEx(&cfg, bf16 ? router_loss_kernel<true, W, true> : router_loss_kernel<false, W, true>, a, part,
+                                vec);
+    return cudaLaunchKernelEx(&cfg, bf16 ? router_loss_kernel<true, W, false> : router_loss_kernel<false, W, false>, a, part,
+                              vec);
+  });
+  if (e != cudaSuccess) return e;
+  count_launch();
+  if (one) return cudaSuccess;
   router_loss_finish_kernel<<<RF_CLUSTER, RF_THREADS, 0, st>>>(a, part, int(blocks));
   count_launch();
   return cudaGetLastError();
