@@ -154,18 +154,27 @@ __global__ void __launch_bounds__(PB) perm_scatter_kernel(const int32_t* __restr
 // All passes at once for at most PB slots (a decoding batch), in one CTA: the
 // same results from one launch instead of five (two fills, histogram, scan,
 // scatter), whose launches would take longer than their work: 8 slots of 128
-// experts took 21.5 us between events, now 8.0 (events alone: 3).
+// experts took 21.5 us between events, now 8.0 (events alone: 3).  CTA 0 sorts and
+// fills the rows that groups can reach; the others fill the row maps behind them.
 __global__ void __launch_bounds__(PB) perm_small_kernel(const int32_t* __restrict__ idx,
                                                         const float* __restrict__ prob, int32_t R, int32_t E,
-                                                        int64_t rows_cap, int32_t* __restrict__ split,
+                                                        int64_t rows_cap, int64_t reach, int32_t* __restrict__ split,
                                                         int32_t* __restrict__ offs, int32_t* __restrict__ slot_to_row,
                                                         int32_t* __restrict__ row_to_slot,
                                                         float* __restrict__ prob_perm) {
   release_dependents();
   dependency_wait(idx, prob);
-  extern __shared__ int wcnt[];  // [32 warps][E]: counts, then first ranks; then [E + 1] group offsets
+  extern __shared__ int wcnt[];  // [warps with slots][E]: counts, then first ranks; then [E] group offsets
   __shared__ int wsum[MOE_MAX_EXPERTS / 32];
-  int* goff = wcnt + 32 * E;
+  if (blockIdx.x > 0) {
+    for (int64_t i = reach + int64_t(blockIdx.x - 1) * PB + threadIdx.x; i < rows_cap; i += int64_t(gridDim.x - 1) * PB) {
+      row_to_slot[i] = -1;
+      prob_perm[i] = 0.0f;
+    }
+    return;
+  }
+  const int nw = (R + 31) >> 5;  // warps with slots
+  int* goff = wcnt + nw * E;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int32_t e = -1;
   if (tid < R) {
@@ -175,21 +184,24 @@ __global__ void __launch_bounds__(PB) perm_small_kernel(const int32_t* __restric
       e = -1;
     }
   }
-  for (int i = tid; i < 32 * E; i += PB) wcnt[i] = 0;
-  for (int64_t i = tid; i < rows_cap; i += PB) {
+  for (int i = tid; i < nw * E; i += PB) wcnt[i] = 0;
+  for (int64_t i = tid; i < reach; i += PB) {
     row_to_slot[i] = -1;
     prob_perm[i] = 0.0f;
   }
   __syncthreads();
-  const uint32_t mask = __match_any_sync(0xFFFFFFFFu, e);
-  const uint32_t lrank = __popc(mask & ((1u << lane) - 1u));
-  if (e >= 0 && lrank == 0) wcnt[warp * E + e] = __popc(mask);
+  uint32_t lrank = 0;
+  if (warp < nw) {
+    const uint32_t mask = __match_any_sync(0xFFFFFFFFu, e);
+    lrank = __popc(mask & ((1u << lane) - 1u));
+    if (e >= 0 && lrank == 0) wcnt[warp * E + e] = __popc(mask);
+  }
   __syncthreads();
   // thread x: expert x's slots before each warp's, its total and its padded rows
   int32_t total = 0, padded = 0;
   if (tid < MOE_MAX_EXPERTS) {
     if (tid < E) {
-      for (int w = 0; w < 32; ++w) {
+      for (int w = 0; w < nw; ++w) {
         const int32_t c = wcnt[w * E + tid];
         wcnt[w * E + tid] = total;
         total += c;
@@ -234,7 +246,7 @@ __global__ void __launch_bounds__(PB) perm_small_kernel(const int32_t* __restric
 // permuted order).  FMT: y holds bf16 rows (COMBINE_BF16), fp32 rows
 // (COMBINE_F32) or f24 rows (COMBINE_F24: the top 3 bytes of each fp32
 // value, see common.cuh).
-template <int FMT>
+template <int FMT, int U>
 __global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ yv, const int32_t* __restrict__ slot_to_row,
                                                       int64_t T, int32_t k, int64_t H8, uint4* __restrict__ out) {
   release_dependents();
@@ -244,28 +256,53 @@ __global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ y
        i += int64_t(gridDim.x) * blockDim.x) {
     const int64_t t = i / H8, c = i % H8;
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int j = 0; j < k; ++j) {
-      const int64_t row = slot_to_row ? int64_t(__ldg(slot_to_row + t * k + j)) : t * k + j;
-      if (row < 0) continue;  // a slot whose expert id was rejected
-      if constexpr (FMT == COMBINE_F32) {
-        const float4* y = static_cast<const float4*>(yv) + (row * H8 + c) * 2;
-        const float4 v0 = __ldg(y), v1 = __ldg(y + 1);
-        acc[0] += v0.x; acc[1] += v0.y; acc[2] += v0.z; acc[3] += v0.w;
-        acc[4] += v1.x; acc[5] += v1.y; acc[6] += v1.z; acc[7] += v1.w;
-      } else if constexpr (FMT == COMBINE_F24) {
-        const uint2* y = static_cast<const uint2*>(yv) + (row * H8 + c) * 3;  // 24 bytes: 8 values
-        const uint2 a = __ldg(y), b = __ldg(y + 1), d = __ldg(y + 2);
-        uint32_t f[8];
-        f24_unpack4(a.x, a.y, b.x, f);
-        f24_unpack4(b.y, d.x, d.y, f + 4);
+    // U choices at a time, all their loads in flight, added in order
+    for (int j0 = 0; j0 < k; j0 += U) {
+      int64_t row[U];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += __uint_as_float(f[e]);
-      } else {
-        const uint4 v = __ldg(static_cast<const uint4*>(yv) + row * H8 + c);
-        acc[0] += bf16lo(v.x); acc[1] += bf16hi(v.x);
-        acc[2] += bf16lo(v.y); acc[3] += bf16hi(v.y);
-        acc[4] += bf16lo(v.z); acc[5] += bf16hi(v.z);
-        acc[6] += bf16lo(v.w); acc[7] += bf16hi(v.w);
+      for (int j = 0; j < U; ++j)
+        row[j] = j0 + j >= k ? -1 : (slot_to_row ? int64_t(__ldg(slot_to_row + t * k + j0 + j)) : t * k + j0 + j);
+      constexpr int W = FMT == COMBINE_F32 ? 8 : (FMT == COMBINE_F24 ? 6 : 4);  // words of eight values
+      uint32_t w[U][W];
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        if (row[j] < 0) continue;  // past k, or a slot whose expert id was rejected
+        if constexpr (FMT == COMBINE_F24) {
+          const uint2* y = static_cast<const uint2*>(yv) + (row[j] * H8 + c) * 3;
+#pragma unroll
+          for (int x = 0; x < 3; ++x) {
+            const uint2 v = __ldg(y + x);
+            w[j][2 * x] = v.x;
+            w[j][2 * x + 1] = v.y;
+          }
+        } else {
+          const uint4* y = static_cast<const uint4*>(yv) + (row[j] * H8 + c) * (W / 4);
+#pragma unroll
+          for (int x = 0; x < W / 4; ++x) {
+            const uint4 v = __ldg(y + x);
+            w[j][4 * x] = v.x; w[j][4 * x + 1] = v.y; w[j][4 * x + 2] = v.z; w[j][4 * x + 3] = v.w;
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        if (row[j] < 0) continue;
+        if constexpr (FMT == COMBINE_F32) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] += __uint_as_float(w[j][e]);
+        } else if constexpr (FMT == COMBINE_F24) {
+          uint32_t f[8];
+          f24_unpack4(w[j][0], w[j][1], w[j][2], f);
+          f24_unpack4(w[j][3], w[j][4], w[j][5], f + 4);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] += __uint_as_float(f[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc[2 * e] += bf16lo(w[j][e]);
+            acc[2 * e + 1] += bf16hi(w[j][e]);
+          }
+        }
       }
     }
     out[i] = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
@@ -295,8 +332,12 @@ cudaError_t launch_permute_index(const int32_t* idx, const float* prob, int64_t 
                                  int32_t* row_to_slot, int32_t* slot_to_row, float* prob_perm,
                                  void* ws, cudaStream_t st) {
   if (R > 0 && R <= PB) {
-    return launch_dependent(perm_small_kernel, 1, PB, 33 * E * sizeof(int), st, idx, prob, int32_t(R), E, rows_cap, split,
-                            offs, slot_to_row, row_to_slot, prob_perm);
+    // no more groups than experts or slots, each within one 128-row tile but for
+    // every 128 slots one tile more
+    const int64_t most = 128 * ((R < E ? R : int64_t(E)) + R / 128), reach = most < rows_cap ? most : rows_cap;
+    const unsigned fill = unsigned(cdiv(rows_cap - reach, 4 * PB));
+    return launch_dependent(perm_small_kernel, 1 + fill, PB, (cdiv(R, 32) + 1) * E * sizeof(int), st, idx, prob,
+                            int32_t(R), E, rows_cap, reach, split, offs, slot_to_row, row_to_slot, prob_perm);
   }
   // (an empty batch too: one block, no slots)
   const int32_t nb = int32_t(cdiv(R, PB));
@@ -313,8 +354,16 @@ cudaError_t launch_combine(const void* y, int fmt, const int32_t* slot_to_row, i
   int64_t blocks = cdiv(n, 256);
   if (blocks > 148 * 32) blocks = 148 * 32;
   uint4* o = static_cast<uint4*>(out);
-  auto kern = fmt == COMBINE_F32 ? combine_kernel<COMBINE_F32>
-                                 : (fmt == COMBINE_F24 ? combine_kernel<COMBINE_F24> : combine_kernel<COMBINE_BF16>);
+  // Four choices in flight where a small batch leaves the SMs without enough warps
+  // to cover the loads' latency (64 tokens, k = 4: 9.2 -> 7.9 us between events);
+  // with enough of them the registers cost more (8192 x 4096, k = 2: 48.8 -> 58.8)
+  auto pick = [&](auto U) {
+    constexpr int u = decltype(U)::value;
+    return fmt == COMBINE_F32 ? combine_kernel<COMBINE_F32, u>
+                              : (fmt == COMBINE_F24 ? combine_kernel<COMBINE_F24, u> : combine_kernel<COMBINE_BF16, u>);
+  };
+  const bool few = blocks <= int64_t(device_sm_count()) * 4;
+  auto kern = few ? pick(std::integral_constant<int, 4>()) : pick(std::integral_constant<int, 1>());
   return launch_dependent(kern, unsigned(blocks), 256, 0, st, y, slot_to_row, T, k, H / 8, o);
 }
 

@@ -1,5 +1,7 @@
 // Launch interfaces of the permutation and combine kernels.
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace moe {
