@@ -116,6 +116,12 @@ __device__ __forceinline__ void store_row8(void* p, int t, int E, int g, bool ve
   }
 }
 
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const void* p, int64_t i) {
+  if constexpr (BF16) return __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(p) + i)) << 16);
+  return __ldg(static_cast<const float*>(p) + i);
+}
+
 // Sum and maximum over the G lanes of a group, the same in each of them.
 template <int G>
 __device__ __forceinline__ float group_sum(float x) {
@@ -523,6 +529,213 @@ __global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM<G>)
   }
 }
 
+// Three to eight kept experts of more than 64: sixteen lanes own a token, V
+// consecutive experts each (8 for E <= 128, else 16), so that a warp works on
+// two tokens and what is not per expert -- the probabilities, the sums'
+// exchanges -- costs half of what it does with 32 lanes.
+// Selection without rounds: at least k experts reach the k-th largest of the
+// lanes' maxima, so a bitonic sort of the sixteen maxima (ten exchanges) gives a
+// threshold that about ten of 256 random logits pass for k = 8.  Those go to a
+// list in ascending order of their ids, one lane takes each, and its place among
+// the kept ones is the number of entries that come before it: larger, or equal
+// and earlier in the list.  More than 16 entries (0.8 % of tokens with 256
+// random logits) are two per lane; more than 32, as with many equal logits, are
+// kept in k rounds over all logits.
+// 262144 tokens, this kernel against the one above: 256 experts, k = 8 119 / 185
+// us, k = 4 119 / 141, k = 2 118 / 123; 128 experts, k = 8 92 / 142, k = 1 87 / 73
+// -- the work does not grow with k here, so k = 1 and 2 stay with the rounds.  Bound by
+// instruction issue; three blocks per SM (no spills) or the next row's logits on
+// their way measured the same or slower.
+constexpr int TOP_LANES = 16, TOP_K_MIN = 3, TOP_K = 8, TOP_LIST = 32, TOP_BLOCKS_PER_SM = 4;
+
+template <bool BF16, int V>
+__global__ void __launch_bounds__(RL_THREADS, TOP_BLOCKS_PER_SM)
+    router_loss_top8_kernel(const RouterLossArgs a, const LossPartials part, const bool vec) {
+  constexpr int G = TOP_LANES, GROUPS = 32 / G, E_MAX = G * V;
+  __shared__ float2 list[RL_WARPS * GROUPS][TOP_K + 1];  // (value, id as bits) of a token's kept experts, in order
+  __shared__ uint8_t ids[RL_WARPS * GROUPS][TOP_LIST];   // experts that reach the threshold
+  __shared__ float bsum[RL_WARPS][E_MAX];
+  __shared__ int32_t bcnt[E_MAX];
+  __shared__ float bz[RL_WARPS];
+  __shared__ int32_t bn[RL_WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane & (G - 1), sub = lane / G;
+  const int slot = warp * GROUPS + sub;
+  const int E = a.E, k = a.k;
+  for (int e = threadIdx.x; e < E_MAX; e += RL_THREADS) bcnt[e] = 0;
+  __syncthreads();
+  // bits of the numbers that are experts
+  const int have = min(max(E - V * g, 0), V);
+  const uint32_t some = (1u << have) - 1u;
+  float acc[V], zsum = 0.0f;
+  int32_t n = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+  constexpr int per = RL_WARPS * GROUPS;
+  const int step = int(gridDim.x) * per;
+  int t0 = int(blockIdx.x) * per + warp * GROUPS;
+  for (; t0 < a.T; t0 += step) {
+    const bool in = t0 + sub < a.T;
+    const int t = in ? t0 + sub : a.T - 1;
+    float v[V];
+    const bool live = in && (!a.mask || a.mask[t] != 0);
+#pragma unroll
+    for (int h = 0; h < V / 8; ++h) load_row8<BF16>(a.logits, t, E, V / 8 * g + h, vec, v + 8 * h);
+    float x = neg_inf();
+#pragma unroll
+    for (int i = 0; i < V; ++i) x = fmaxf(x, v[i]);  // passes over NaN
+#pragma unroll
+    for (int size = 2; size <= G; size *= 2)
+#pragma unroll
+      for (int d = size / 2; d >= 1; d /= 2) {
+        const float y = __shfl_xor_sync(0xFFFFFFFFu, x, d);
+        x = ((g & d) == 0) == ((g & size) == 0) ? fmaxf(x, y) : fminf(x, y);
+      }
+    const float m = __shfl_sync(0xFFFFFFFFu, x, 0, G), least = __shfl_sync(0xFFFFFFFFu, x, k - 1, G);
+    // softmax over all experts, as in the kernel above
+    const float ml = m * LOG2E;
+    float ex[V], se = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      ex[i] = fast_exp2(fmaf(v[i], LOG2E, -ml));
+      se += ex[i];
+    }
+    if (se != se) {  // NaN (or infinities) among the lane's logits
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (v[i] != v[i]) v[i] = neg_inf();  // NaN ranks last
+    }
+    se = group_sum<G>(se);
+    const float lse = live ? m + __logf(se) : 0.0f;
+    if (in && g == 0) a.lse[t] = lse;
+    if (live) {
+      const float inv = __fdividef(1.0f, se);
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = fmaf(ex[i], inv, acc[i]);
+      if (g == 0) {
+        zsum += lse * lse;
+        n += 1;
+      }
+    }
+    uint32_t reach = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) reach |= v[i] >= least ? 1u << i : 0u;
+    reach &= some;
+    const int own = __popc(reach);
+    int upto = own;
+#pragma unroll
+    for (int d = 1; d < G; d *= 2) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, upto, d, G);
+      if (g >= d) upto += y;
+    }
+    const int total = __shfl_sync(0xFFFFFFFFu, upto, G - 1, G);
+    auto keep = [&](int r, float value, int id) {
+      list[slot][r] = make_float2(value, __int_as_float(id));
+      if (live) atomicAdd(&bcnt[id], 1);
+    };
+    if (!__any_sync(0xFFFFFFFFu, total > TOP_LIST)) {
+      for (int at = upto - own; reach != 0; reach &= reach - 1u) ids[slot][at++] = uint8_t(V * g + __ffs(int(reach)) - 1);
+      const bool more = __any_sync(0xFFFFFFFFu, total > G);
+      __syncwarp();
+      float value[2];
+      int id[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        value[h] = __int_as_float(0x7FC00000);  // no entry: before nothing
+        id[h] = 0;
+        if (g + h * G < total) {
+          id[h] = ids[slot][g + h * G];
+          value[h] = fmaxf(load_logit<BF16>(a.logits, int64_t(t) * E + id[h]), neg_inf());
+        }
+      }
+      int rank = 0;
+      auto before = [&](float w, int jpos, float mine, int pos) { return w > mine || (w == mine && jpos < pos); };
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        if (j == 12 && !__any_sync(0xFFFFFFFFu, total > j)) break;
+        rank += before(__shfl_sync(0xFFFFFFFFu, value[0], j, G), j, value[0], g);
+      }
+      if (more) {
+        int rank1 = 0;
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+          const float w0 = __shfl_sync(0xFFFFFFFFu, value[0], j, G), w1 = __shfl_sync(0xFFFFFFFFu, value[1], j, G);
+          rank += w1 > value[0];
+          rank1 += (w0 >= value[1]) + before(w1, j, value[1], g);
+        }
+        if (g + G < total && rank1 < k) keep(rank1, value[1], id[1]);
+      }
+      if (g < total && rank < k) keep(rank, value[0], id[0]);
+    } else {
+      uint32_t left = some;
+      for (int r = 0; r < k; ++r) {
+        float best = __int_as_float(0x7FC00000);
+        int who = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (((left >> i) & 1u) && !(v[i] <= best)) {
+            best = v[i];
+            who = i;
+          }
+        const float top = group_max<G>(best);
+        // the lowest of the group's lanes that hold the maximum
+        const uint32_t hold = __ballot_sync(0xFFFFFFFFu, best == top) >> (sub * G) & ((1u << G) - 1u);
+        if (g == __ffs(int(hold)) - 1) {
+          keep(r, best, V * g + who);
+          left &= ~(1u << who);
+        }
+      }
+    }
+    __syncwarp();
+    // probabilities of the kept experts, kept expert r in lane r: the sum's order
+    // is the butterfly over 32 places of moe_router_topk, whose others are 0
+    float p = 0.0f;
+    int id = 0;
+    if (g < k) {
+      const float2 y = list[slot][g];
+      p = expf(y.x - m);
+      id = __float_as_int(y.y);
+    }
+    const float psum = group_sum<TOP_K>(p);
+    if (in && g < k) {
+      a.topk_idx[int64_t(t) * k + g] = id;
+      a.topk_prob[int64_t(t) * k + g] = live ? p / psum : 0.0f;
+    }
+    __syncwarp();  // the list is read before the next token's is written
+  }
+  // the block's sums: over the warp's two groups by shuffles, over the warps in order
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] += __shfl_xor_sync(0xFFFFFFFFu, acc[i], G);
+  zsum += __shfl_xor_sync(0xFFFFFFFFu, zsum, G);
+  n += __shfl_xor_sync(0xFFFFFFFFu, n, G);
+  if (sub == 0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) bsum[warp][V * g + i] = acc[i];
+    if (g == 0) {
+      bz[warp] = zsum;
+      bn[warp] = n;
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += RL_THREADS) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < RL_WARPS; ++w) s += bsum[w][e];
+    part.sums[int64_t(blockIdx.x) * E + e] = s;
+    part.counts[int64_t(blockIdx.x) * E + e] = bcnt[e];
+  }
+  if (threadIdx.x == 0) {
+    float z = 0.0f;
+    int32_t c = 0;
+    for (int w = 0; w < RL_WARPS; ++w) {
+      z += bz[w];
+      c += bn[w];
+    }
+    part.z[blockIdx.x] = z;
+    part.n[blockIdx.x] = c;
+  }
+}
+
 // Gradient of the logits, on the same lanes.  The k kept logits' gradients are
 // scattered to a zeroed row of shared memory, from which every lane adds its
 // eight; only where a token lists an expert twice are they added one by one.
@@ -684,6 +897,12 @@ unsigned loss_blocks(int32_t T, int32_t E) {
   return unsigned(want < cap ? want : cap);
 }
 
+unsigned top8_blocks(int32_t T) {
+  const int64_t want = cdiv(int64_t(T), int64_t(RL_WARPS) * (32 / TOP_LANES));
+  const int64_t cap = int64_t(device_sm_count()) * TOP_BLOCKS_PER_SM;
+  return unsigned(want < cap ? want : cap);
+}
+
 // rows start on 16-byte boundaries and hold whole runs of eight experts
 bool rows_vectorised(const void* p, const void* q, int32_t E) {
   return E % 8 == 0 && ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & 15u) == 0;
@@ -703,13 +922,23 @@ cudaError_t launch_router_losses(const RouterLossArgs& a, bool bf16, void* ws, c
   // of four experts: 8.4 us, two launches 10.4); more passes take longer than the
   // second launch
   const bool one = a.T <= 2 * RF_CLUSTER * RL_WARPS * (32 / group_width(a.E));
-  const unsigned blocks = one ? RF_CLUSTER : loss_blocks(a.T, a.E);
+  const bool top8 = !one && a.E > 64 && a.k >= TOP_K_MIN && a.k <= TOP_K;
+  const unsigned blocks = one ? RF_CLUSTER : top8 ? top8_blocks(a.T) : loss_blocks(a.T, a.E);
   LossPartials part;
   part.sums = static_cast<float*>(ws);
   part.counts = reinterpret_cast<int32_t*>(part.sums + int64_t(blocks) * a.E);
   part.z = reinterpret_cast<float*>(part.counts + int64_t(blocks) * a.E);
   part.n = reinterpret_cast<int32_t*>(part.z + blocks);
   const bool vec = rows_vectorised(a.logits, a.logits, a.E);
+  if (top8) {
+    const auto kernel = a.E <= 8 * TOP_LANES ? (bf16 ? router_loss_top8_kernel<true, 8> : router_loss_top8_kernel<false, 8>)
+                                             : (bf16 ? router_loss_top8_kernel<true, 16> : router_loss_top8_kernel<false, 16>);
+    kernel<<<blocks, RL_THREADS, 0, st>>>(a, part, vec);
+    count_launch();
+    router_loss_finish_kernel<<<RF_CLUSTER, RF_THREADS, 0, st>>>(a, part, int(blocks));
+    count_launch();
+    return cudaGetLastError();
+  }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = RF_CLUSTER;

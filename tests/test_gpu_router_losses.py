@@ -134,6 +134,63 @@ def test_workload_logits(name):
     _run(z, cfg.k, mask=mask)
 
 
+@pytest.mark.parametrize("E", [65, 72, 100, 128, 129, 136, 200, 256])
+@pytest.mark.parametrize("k", [3, 5, 8])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_many_experts_with_few_kept(E, k, bf16):
+    rng = np.random.default_rng(E * k)
+    _run(rng.normal(size=(601, E)) * 2 + rng.normal(size=E), k, bf16=bf16, mask=rng.random(601) < 0.9)
+
+
+@pytest.mark.parametrize("E", [96, 250])
+@pytest.mark.parametrize("kind", ["all equal", "two values", "five values", "rising", "falling", "one lane", "minus infinity",
+                                  "zeros of both signs"])
+def test_many_experts_with_ties(E, kind):
+    rng = np.random.default_rng(E)
+    T = 515
+    z = {"all equal": lambda: np.full((T, E), 0.25),
+         "two values": lambda: rng.integers(0, 2, (T, E)) * 1.0,
+         "five values": lambda: rng.integers(0, 5, (T, E)) * 0.5,
+         "rising": lambda: np.tile(np.arange(E) / 16.0, (T, 1)),
+         "falling": lambda: np.tile(-np.arange(E) / 16.0, (T, 1)),
+         "one lane": lambda: np.where(np.arange(E)[None, :] // 16 == rng.integers(0, E // 16, (T, 1)), 4.0, 0.0)
+                             + np.round(rng.normal(size=(T, E)) * 4) / 4,
+         "minus infinity": lambda: np.where(rng.random((T, E)) < 0.97, -np.inf, rng.normal(size=(T, E))),
+         "zeros of both signs": lambda: np.where(rng.random((T, E)) < 0.5, 0.0, -0.0)}[kind]()
+    if kind == "minus infinity":
+        z[:, 3] = 0.0  # no row without a finite logit
+    _run(z, 7)
+
+
+@pytest.mark.parametrize("k", [4, 8])
+def test_many_experts_with_odd_logits_behind_the_mask(k):
+    rng = np.random.default_rng(k)
+    T, E = 700, 200
+    z = rng.normal(size=(T, E))
+    mask = rng.random(T) < 0.5
+    bad = np.flatnonzero(~mask)
+    z[bad[0::4]] = np.nan
+    z[bad[1::4]] = np.inf
+    z[bad[2::4]] = -np.inf
+    z[bad[3::4], ::3] = np.nan
+    _run(z, k, mask=mask)
+
+
+@pytest.mark.parametrize("E,k", [(128, 8), (256, 8), (256, 3), (100, 4)])
+def test_many_tokens_same_bits_as_the_plain_router(E, k):
+    import torch
+    T = 20011  # several tokens for every group of lanes
+    z = _device(np.random.default_rng(E + k).normal(size=(T, E)) * 2)
+    layer = _layer(T, E, k)
+    idx, prob, losses = layer.route_losses(z)
+    idx, prob, losses, counts = idx.clone(), prob.clone(), losses.clone(), layer.expert_counts.clone()
+    i2, p2 = layer.route(z)
+    assert torch.equal(idx, i2) and torch.equal(prob, p2)
+    assert torch.equal(counts.long(), torch.bincount(idx.flatten().long(), minlength=E))
+    _, _, again = layer.route_losses(z)
+    assert torch.equal(losses, again)
+
+
 def test_ties():
     rng = np.random.default_rng(5)
     z = np.round(rng.normal(size=(999, 40)) * 2) / 2
