@@ -173,6 +173,7 @@ class GroupedMLP:
         self.xq_col = self.xq_col_sf = None   # x along tokens: only when permute(..., with_cols=True)
         self._x = None                         # the input of the last permutation (the backward's x)
         self.router_lse = None                 # route_losses' outputs, once it has run
+        self.dlogits = {}                      # route_backward's, one buffer per type it has met
         self.w1q4 = None                       # MXFP4 weights, once quantised or loaded
 
     def _need_mxfp8(self):
@@ -322,7 +323,7 @@ class GroupedMLP:
         """Gradient of the logits (moe_router_bwd) after route_losses on the
         same logits and mask: dprob fp32 [T, k] (as backward() returns it)
         and dlosses fp32 [2], either None for zero -> dlogits [T, E] in the
-        logits' type, in a buffer of this layer."""
+        logits' type, in a buffer of this layer (one per type)."""
         T, E, k = self.T, self.E, self.k
         dt = _logits_dtype(logits)
         check_tensor(logits, "logits", logits.dtype, (T, E), self.dev)
@@ -334,14 +335,14 @@ class GroupedMLP:
             check_tensor(dlosses, "dlosses", torch.float32, (2,), self.dev)
         if token_mask is not None:
             check_tensor(token_mask, "token_mask", torch.bool, (T,), self.dev)
-        if getattr(self, "dlogits", None) is None or self.dlogits.dtype != logits.dtype:
-            self.dlogits = self._alloc.typed((T, E), logits.dtype, "dlogits")
+        if logits.dtype not in self.dlogits:
+            self.dlogits[logits.dtype] = self._alloc.typed((T, E), logits.dtype, "dlogits")
+        dlogits = self.dlogits[logits.dtype]
         with on_device(self.dev):
             lib.moe_router_bwd(logits.data_ptr(), dt, T, E, k, _ptr(token_mask), _ptr(self.topk_idx),
                                _ptr(self.topk_prob), _ptr(self.router_lse), _ptr(self.expert_counts),
-                               _ptr(self.routed_tokens), _ptr(dprob), _ptr(dlosses), _ptr(self.dlogits),
-                               self._stream())
-        return self.dlogits
+                               _ptr(self.routed_tokens), _ptr(dprob), _ptr(dlosses), _ptr(dlogits), self._stream())
+        return dlogits
 
     def _mxfp4_weights(self):
         if self.w1q4 is None:
