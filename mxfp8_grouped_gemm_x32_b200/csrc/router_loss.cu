@@ -538,9 +538,10 @@ __global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM<G>)
 // threshold that about ten of 256 random logits pass for k = 8.  Those go to a
 // list in ascending order of their ids, one lane takes each, and its place among
 // the kept ones is the number of entries that come before it: larger, or equal
-// and earlier in the list.  More than 16 entries (0.8 % of tokens with 256
-// random logits) are two per lane; more than 32, as with many equal logits, are
-// kept in k rounds over all logits.
+// and earlier in the list.  Where more than 16 pass (0.8 % of tokens with 256
+// random logits, and rows of equal ones, as padding has them) only the first k of
+// those that equal the threshold stay; more than 16 entries are two per lane, more
+// than 32 (sixteen large logits in a row) are kept in k rounds over all logits.
 // 262144 tokens, this kernel against the one above: 256 experts, k = 8 119 / 185
 // us, k = 4 119 / 141, k = 2 118 / 123; 128 experts, k = 8 92 / 142, k = 1 87 / 73
 // -- the work does not grow with k here, so k = 1 and 2 stay with the rounds.  Bound by
@@ -621,20 +622,40 @@ __global__ void __launch_bounds__(RL_THREADS, TOP_BLOCKS_PER_SM)
 #pragma unroll
     for (int i = 0; i < V; ++i) reach |= v[i] >= least ? 1u << i : 0u;
     reach &= some;
-    const int own = __popc(reach);
-    int upto = own;
+    int upto, total;  // entries of the group's lanes up to this one, and of all
+    auto count = [&] {
+      upto = __popc(reach);
 #pragma unroll
-    for (int d = 1; d < G; d *= 2) {
-      const int y = __shfl_up_sync(0xFFFFFFFFu, upto, d, G);
-      if (g >= d) upto += y;
+      for (int d = 1; d < G; d *= 2) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, upto, d, G);
+        if (g >= d) upto += y;
+      }
+      total = __shfl_sync(0xFFFFFFFFu, upto, G - 1, G);
+    };
+    count();
+    if (__any_sync(0xFFFFFFFFu, total > G)) {
+      // equal logits (padding's): of those that equal the threshold the first k suffice
+      const uint32_t above = [&] {
+        uint32_t w = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) w |= v[i] > least ? 1u << i : 0u;
+        return w & some;
+      }();
+      uint32_t equal = reach & ~above;
+      reach = equal;
+      count();
+      int spare = k - (upto - __popc(equal));  // places left after the lanes before this one
+      uint32_t drop = equal;
+      for (; drop != 0 && spare > 0; --spare) drop &= drop - 1u;
+      reach = above | (equal & ~drop);
+      count();
     }
-    const int total = __shfl_sync(0xFFFFFFFFu, upto, G - 1, G);
     auto keep = [&](int r, float value, int id) {
       list[slot][r] = make_float2(value, __int_as_float(id));
       if (live) atomicAdd(&bcnt[id], 1);
     };
     if (!__any_sync(0xFFFFFFFFu, total > TOP_LIST)) {
-      for (int at = upto - own; reach != 0; reach &= reach - 1u) ids[slot][at++] = uint8_t(V * g + __ffs(int(reach)) - 1);
+      for (int at = upto - __popc(reach); reach != 0; reach &= reach - 1u) ids[slot][at++] = uint8_t(V * g + __ffs(int(reach)) - 1);
       const bool more = __any_sync(0xFFFFFFFFu, total > G);
       __syncwarp();
       float value[2];

@@ -143,8 +143,8 @@ def test_many_experts_with_few_kept(E, k, bf16):
 
 
 @pytest.mark.parametrize("E", [96, 250])
-@pytest.mark.parametrize("kind", ["all equal", "two values", "five values", "rising", "falling", "one lane", "minus infinity",
-                                  "zeros of both signs"])
+@pytest.mark.parametrize("kind", ["all equal", "two values", "five values", "rising", "falling", "one lane", "two lanes",
+                                  "minus infinity", "zeros of both signs", "zero rows"])
 def test_many_experts_with_ties(E, kind):
     rng = np.random.default_rng(E)
     T = 515
@@ -155,6 +155,9 @@ def test_many_experts_with_ties(E, kind):
          "falling": lambda: np.tile(-np.arange(E) / 16.0, (T, 1)),
          "one lane": lambda: np.where(np.arange(E)[None, :] // 16 == rng.integers(0, E // 16, (T, 1)), 4.0, 0.0)
                              + np.round(rng.normal(size=(T, E)) * 4) / 4,
+         "two lanes": lambda: np.where(np.arange(E)[None, :] // 16 % 2 == np.arange(T)[:, None] % 2, 9.0, 0.0)
+                              + rng.normal(size=(T, E)),
+         "zero rows": lambda: np.where(rng.random((T, 1)) < 0.5, 0.0, rng.normal(size=(T, E))),
          "minus infinity": lambda: np.where(rng.random((T, E)) < 0.97, -np.inf, rng.normal(size=(T, E))),
          "zeros of both signs": lambda: np.where(rng.random((T, E)) < 0.5, 0.0, -0.0)}[kind]()
     if kind == "minus infinity":
