@@ -20,18 +20,23 @@
 //   warp 13       the same for the scales (bulk copies), ring of 6 or 8
 //   warp 14       TMEM owner and MMA issuer; a stage is ready when its copies have
 //                 landed and the four scale warps have stored its scales
-// What bounds it, measured on the Mixtral gate_up shape (3.85 TFLOP) with parts
-// left out: in a first version (128 x 256 tiles, one accumulator, scales to TMEM
-// by tcgen05.cp, as the MXFP8 kernel; 1070 us) the copies from global memory cost
-// nothing, the MMAs alone took 1020 us and without the scale copies 690 -- one
-// tcgen05.cp occupies the tensor pipe for some 80 cycles and a K tile needs six,
-// against 4 x 130 for its MMAs; hence the scale warps.  About 1900 cycles per
-// tile went into handing the accumulator over, hence two of 192 columns (an N =
-// 192 MMA takes 97 cycles; 128 columns remain for the stages' scales).  Of what
-// was left the issuing lane's own instructions took the most, 615 cycles per K
-// tile: it now issues four MMAs in 77.  Without any copies the kernel then
-// takes 557 us, with them 643: 40 KB per K tile and SM from L2 at 71 bytes per
-// cycle, which is what bounds it.
+// Mixtral gate_up (3.85 TFLOP) takes 770 us in a burst (5.0 PFLOP/s) and 860 in a
+// long run, where the card's power limit sets the rate; down (1.92 TFLOP) 403.
+// How it came there, on the same shape:
+//   128 x 256 tiles, one accumulator, scales to TMEM by tcgen05.cp (as the MXFP8
+//   kernel): 1070 us.  One tcgen05.cp occupies the tensor pipe for some 80 cycles
+//   and a K tile needs six, against 4 x 130 for its MMAs; hence the scale warps.
+//   Handing the one accumulator over took 1900 cycles per tile, hence two of 192
+//   columns (an N = 192 MMA takes 97 cycles; 128 columns remain for the scales).
+//   The issuing lane's own instructions took 615 cycles per K tile; with
+//   descriptors by addition and barriers looked at ahead it issues four MMAs in 77.
+//   Scales read from global memory by the scale warps: 1052; by bulk copies to
+//   shared memory, a warp of their own for those: 862 (weights' scales eight copies
+//   per K tile); the weights' scales in the order of the tiles, one copy: 783.
+// Without its scales the kernel takes 643, without operand copies as well 557:
+// what bounds it in a burst is 40 KB per K tile and SM from L2, 71 bytes a cycle.
+// CTA pairs (256 x 192, half of B each) read less and were no faster: 808 us, and
+// 1440 against 1454 us for a whole forward in a long run.
 // Every wait is bounded, as in the MXFP8 kernel: on time-out the kernel records
 // MOE_ERR_TIMEOUT, lets its copies and MMAs in flight finish and frees TMEM.
 #include "mxfp4.cuh"

@@ -154,8 +154,9 @@ __global__ void __launch_bounds__(PB) perm_scatter_kernel(const int32_t* __restr
 // All passes at once for at most PB slots (a decoding batch), in one CTA: the
 // same results from one launch instead of five (two fills, histogram, scan,
 // scatter), whose launches would take longer than their work: 8 slots of 128
-// experts took 21.5 us between events, now 8.0 (events alone: 3).  CTA 0 sorts and
-// fills the rows that groups can reach; the others fill the row maps behind them.
+// experts took 21.5 us between events, now 5.9 (events alone: 3).  CTA 0 sorts and
+// fills the rows that groups can reach; the others fill the row maps behind them
+// (8.0 us when CTA 0 filled them all).
 __global__ void __launch_bounds__(PB) perm_small_kernel(const int32_t* __restrict__ idx,
                                                         const float* __restrict__ prob, int32_t R, int32_t E,
                                                         int64_t rows_cap, int64_t reach, int32_t* __restrict__ split,
