@@ -211,17 +211,18 @@ struct LossPartials {
   int32_t* n;       // [blocks]
 };
 
-// Sum over the block in a fixed order, the same in every thread.
+// Sum over the block in a fixed order, in thread 0 (the others get anything).
+__device__ __forceinline__ double warp_sum(double x) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
+  return x;
+}
 template <int THREADS>
-__device__ __forceinline__ double block_sum(double x, double* buf) {
+__device__ __forceinline__ double block_sum(double x, double* warps) {
+  x = warp_sum(x);
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = x;
   __syncthreads();
-  buf[threadIdx.x] = x;
-  __syncthreads();
-  for (int s = THREADS / 2; s >= 1; s >>= 1) {
-    if (int(threadIdx.x) < s) buf[threadIdx.x] += buf[threadIdx.x + s];
-    __syncthreads();
-  }
-  return buf[0];
+  return warp_sum(int(threadIdx.x) < THREADS / 32 ? warps[threadIdx.x] : 0.0);
 }
 
 __device__ __forceinline__ double ld_cluster_f64(const double* p, uint32_t rank) {
@@ -235,11 +236,12 @@ struct FinishShared {
   double buf[THREADS];
   int32_t ibuf[THREADS];
   double sums[MOE_MAX_EXPERTS], counts[MOE_MAX_EXPERTS];  // this block's
+  double zw[32], nw[32], dw[32];                          // of its warps
   double z, n;
 };
 
 // The cluster's blocks add the rows of partial sums up, block c the rows c, c + 8,
-// ..., four loads in flight per thread; block 0 then adds the blocks' sums, in
+// ..., eight rows in flight per thread; block 0 then adds the blocks' sums, in
 // order, and writes the results.  Sums in 64 bits (counts too, exactly): a few
 // hundred terms of any size, and no cost next to the loads.
 template <int THREADS>
@@ -251,18 +253,19 @@ __device__ __forceinline__ void finish_losses(const RouterLossArgs& a, const Los
   const int e = tid & (width - 1), slice = tid / width, slices = THREADS / width;
   double s = 0.0;
   int32_t cnt = 0;
+  constexpr int U = 8;
   if (e < a.E)
-    for (int b0 = c + RF_CLUSTER * slice; b0 < blocks; b0 += 4 * RF_CLUSTER * slices) {
-      float x[4];
-      int32_t y[4];
+    for (int b0 = c + RF_CLUSTER * slice; b0 < blocks; b0 += U * RF_CLUSTER * slices) {
+      float x[U];
+      int32_t y[U];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < U; ++i) {
         const int b = b0 + i * RF_CLUSTER * slices;
         x[i] = b < blocks ? part.sums[int64_t(b) * a.E + e] : 0.0f;
         y[i] = b < blocks ? part.counts[int64_t(b) * a.E + e] : 0;
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < U; ++i) {
         s += double(x[i]);
         cnt += y[i];
       }
@@ -285,8 +288,8 @@ __device__ __forceinline__ void finish_losses(const RouterLossArgs& a, const Los
     sh.sums[tid] = s;
     sh.counts[tid] = double(cnt);
   }
-  z = block_sum<THREADS>(z, sh.buf);
-  n = block_sum<THREADS>(n, sh.buf);
+  z = block_sum<THREADS>(z, sh.zw);
+  n = block_sum<THREADS>(n, sh.nw);
   if (tid == 0) {
     sh.z = z;
     sh.n = n;
@@ -305,7 +308,7 @@ __device__ __forceinline__ void finish_losses(const RouterLossArgs& a, const Los
       a.counts[tid] = int32_t(n);
       dot = s * n;
     }
-    dot = block_sum<THREADS>(dot, sh.buf);
+    dot = block_sum<THREADS>(dot, sh.dw);
     if (tid == 0) {
       z = n = 0.0;
       for (int r = 0; r < RF_CLUSTER; ++r) {
