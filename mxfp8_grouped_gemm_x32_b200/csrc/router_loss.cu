@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM<G>)
   }
 }
 
-// Three to eight kept experts of more than 64: sixteen lanes own a token, V
+// Up to eight kept experts of more than 128, three to eight of more than 64: sixteen lanes own a token, V
 // consecutive experts each (8 for E <= 128, else 16), so that a warp works on
 // two tokens and what is not per expert -- the probabilities, the sums'
 // exchanges -- costs half of what it does with 32 lanes.
@@ -545,12 +545,12 @@ __global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM<G>)
 // random logits, and rows of equal ones, as padding has them) only the first k of
 // those that equal the threshold stay; more than 16 entries are two per lane, more
 // than 32 (sixteen large logits in a row) are kept in k rounds over all logits.
-// 262144 tokens, this kernel against the one above: 256 experts, k = 8 119 / 185
-// us, k = 4 119 / 141, k = 2 118 / 123; 128 experts, k = 8 92 / 142, k = 1 87 / 73
-// -- the work does not grow with k here, so k = 1 and 2 stay with the rounds.  Bound by
-// instruction issue; three blocks per SM (no spills) or the next row's logits on
-// their way measured the same or slower.
-constexpr int TOP_LANES = 16, TOP_K_MIN = 3, TOP_K = 8, TOP_LIST = 32, TOP_BLOCKS_PER_SM = 4;
+// 262144 tokens, this kernel against the one above, us: 256 experts k = 8 114 / 182,
+// k = 4 110 / 142, k = 1 108 / 117; 128 experts k = 8 86 / 135, k = 3 83 / 84, k = 2
+// 82 / 76, k = 1 82 / 70 -- the work hardly grows with k here, so k = 1 and 2 stay
+// with the rounds up to 128 experts.  Bound by instruction issue (66 %); three blocks
+// per SM (no spills) or the next row's logits on their way: the same or slower.
+constexpr int TOP_LANES = 16, TOP_K = 8, TOP_LIST = 32, TOP_BLOCKS_PER_SM = 4;
 
 template <bool BF16, int V>
 __global__ void __launch_bounds__(RL_THREADS, TOP_BLOCKS_PER_SM)
@@ -558,6 +558,7 @@ __global__ void __launch_bounds__(RL_THREADS, TOP_BLOCKS_PER_SM)
   constexpr int G = TOP_LANES, GROUPS = 32 / G, E_MAX = G * V;
   __shared__ float2 list[RL_WARPS * GROUPS][TOP_K + 1];  // (value, id as bits) of a token's kept experts, in order
   __shared__ uint8_t ids[RL_WARPS * GROUPS][TOP_LIST];   // experts that reach the threshold
+  __shared__ __align__(16) float vals[RL_WARPS * GROUPS][G];  // the first sixteen of them, their logits
   __shared__ float bsum[RL_WARPS][E_MAX];
   __shared__ int32_t bcnt[E_MAX];
   __shared__ float bz[RL_WARPS];
@@ -672,24 +673,38 @@ __global__ void __launch_bounds__(RL_THREADS, TOP_BLOCKS_PER_SM)
           value[h] = fmaxf(load_logit<BF16>(a.logits, int64_t(t) * E + id[h]), neg_inf());
         }
       }
+      vals[slot][g] = value[0];
+      __syncwarp();
+      // larger entries; equal ones are looked for afterwards, by two that come to
+      // the same place
       int rank = 0;
-      auto before = [&](float w, int jpos, float mine, int pos) { return w > mine || (w == mine && jpos < pos); };
 #pragma unroll
-      for (int j = 0; j < G; ++j) {
+      for (int j = 0; j < G; j += 4) {
         if (j == 12 && !__any_sync(0xFFFFFFFFu, total > j)) break;
-        rank += before(__shfl_sync(0xFFFFFFFFu, value[0], j, G), j, value[0], g);
+        const float4 w = *reinterpret_cast<const float4*>(&vals[slot][j]);
+        rank += (w.x > value[0]) + (w.y > value[0]) + (w.z > value[0]) + (w.w > value[0]);
       }
       if (more) {
         int rank1 = 0;
 #pragma unroll
         for (int j = 0; j < G; ++j) {
-          const float w0 = __shfl_sync(0xFFFFFFFFu, value[0], j, G), w1 = __shfl_sync(0xFFFFFFFFu, value[1], j, G);
+          const float w0 = vals[slot][j], w1 = __shfl_sync(0xFFFFFFFFu, value[1], j, G);
           rank += w1 > value[0];
-          rank1 += (w0 >= value[1]) + before(w1, j, value[1], g);
+          rank1 += (w0 >= value[1]) + (w1 > value[1] || (w1 == value[1] && j < g));
         }
         if (g + G < total && rank1 < k) keep(rank1, value[1], id[1]);
       }
-      if (g < total && rank < k) keep(rank, value[0], id[0]);
+      float2* place = &list[slot][min(rank, TOP_K)];
+      const float2 mine = make_float2(value[0], __int_as_float(id[0]));
+      if (g < total && rank < k) *place = mine;
+      __syncwarp();
+      const bool lost = g < total && rank < k && __float_as_int(place->y) != id[0];
+      if (__any_sync(0xFFFFFFFFu, lost)) {
+#pragma unroll
+        for (int j = 0; j < G; ++j) rank += vals[slot][j] == value[0] && j < g;
+        if (g < total && rank < k) list[slot][rank] = mine;
+      }
+      if (g < total && rank < k && live) atomicAdd(&bcnt[id[0]], 1);
     } else {
       uint32_t left = some;
       for (int r = 0; r < k; ++r) {
@@ -946,7 +961,7 @@ cudaError_t launch_router_losses(const RouterLossArgs& a, bool bf16, void* ws, c
   // of four experts: 8.4 us, two launches 10.4); more passes take longer than the
   // second launch
   const bool one = a.T <= 2 * RF_CLUSTER * RL_WARPS * (32 / group_width(a.E));
-  const bool top8 = !one && a.E > 64 && a.k >= TOP_K_MIN && a.k <= TOP_K;
+  const bool top8 = !one && a.k <= TOP_K && (a.E > 128 || (a.E > 64 && a.k >= 3));
   const unsigned blocks = one ? RF_CLUSTER : top8 ? top8_blocks(a.T) : loss_blocks(a.T, a.E);
   LossPartials part;
   part.sums = static_cast<float*>(ws);

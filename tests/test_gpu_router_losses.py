@@ -135,7 +135,7 @@ def test_workload_logits(name):
 
 
 @pytest.mark.parametrize("E", [65, 72, 100, 128, 129, 136, 200, 256])
-@pytest.mark.parametrize("k", [3, 5, 8])
+@pytest.mark.parametrize("k", [1, 2, 3, 5, 8])
 @pytest.mark.parametrize("bf16", [False, True])
 def test_many_experts_with_few_kept(E, k, bf16):
     rng = np.random.default_rng(E * k)
