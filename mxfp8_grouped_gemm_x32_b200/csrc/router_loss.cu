@@ -90,6 +90,35 @@ __device__ __forceinline__ void load_row8(const void* p, int t, int E, int g, bo
 }
 
 template <bool BF16>
+__device__ __forceinline__ float load_logit(const void* p, int64_t i) {
+  if constexpr (BF16) return __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(p) + i)) << 16);
+  return __ldg(static_cast<const float*>(p) + i);
+}
+
+// Experts V g .. V g + V - 1 of row t, likewise; V is 4 or a multiple of 8.
+template <bool BF16, int V>
+__device__ __forceinline__ void load_row(const void* p, int t, int E, int g, bool vec, float* v) {
+  if constexpr (V >= 8) {
+#pragma unroll
+    for (int h = 0; h < V / 8; ++h) load_row8<BF16>(p, t, E, V / 8 * g + h, vec, v + 8 * h);
+  } else {
+    const int64_t base = int64_t(t) * E + V * g;
+    if (vec && V * g < E) {
+      if constexpr (BF16) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + base));
+        v[0] = bf16lo(w.x); v[1] = bf16hi(w.x); v[2] = bf16lo(w.y); v[3] = bf16hi(w.y);
+      } else {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + base));
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = V * g + i < E ? load_logit<BF16>(p, base + i) : neg_inf();
+    }
+  }
+}
+
+template <bool BF16>
 __device__ __forceinline__ void store_row8(void* p, int t, int E, int g, bool vec, const float* v) {
   const int64_t base = int64_t(t) * E + 8 * g;
   if (8 * g >= E) return;
@@ -114,12 +143,6 @@ __device__ __forceinline__ void store_row8(void* p, int t, int E, int g, bool ve
         if (8 * g + i < E) q[i] = v[i];
     }
   }
-}
-
-template <bool BF16>
-__device__ __forceinline__ float load_logit(const void* p, int64_t i) {
-  if constexpr (BF16) return __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(p) + i)) << 16);
-  return __ldg(static_cast<const float*>(p) + i);
 }
 
 // Sum and maximum over the G lanes of a group, the same in each of them.
@@ -532,8 +555,8 @@ __global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM<G>)
   }
 }
 
-// Up to eight kept experts of more than 128, three to eight of more than 64: sixteen lanes own a token, V
-// consecutive experts each (8 for E <= 128, else 16), so that a warp works on
+// Up to eight kept experts of more than 128, three of more than 64 or five of more than 32: sixteen lanes own a token, V
+// consecutive experts each (4, 8 or 16 by E), so that a warp works on
 // two tokens and what is not per expert -- the probabilities, the sums'
 // exchanges -- costs half of what it does with 32 lanes.
 // Selection without rounds: at least k experts reach the k-th largest of the
@@ -547,8 +570,8 @@ __global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM<G>)
 // than 32 (sixteen large logits in a row) are kept in k rounds over all logits.
 // 262144 tokens, this kernel against the one above, us: 256 experts k = 8 114 / 182,
 // k = 4 110 / 142, k = 1 108 / 117; 128 experts k = 8 86 / 135, k = 3 83 / 84, k = 2
-// 82 / 76, k = 1 82 / 70 -- the work hardly grows with k here, so k = 1 and 2 stay
-// with the rounds up to 128 experts.  Bound by instruction issue (66 %); three blocks
+// 82 / 76, k = 1 82 / 70; 64 experts k = 8 72 / 98, k = 6 71 / 78, k = 4 70 / 62 --
+// the work hardly grows with k here, so few kept of few stay with the rounds.  Bound by instruction issue (66 %); three blocks
 // per SM (no spills) or the next row's logits on their way: the same or slower.
 constexpr int TOP_LANES = 16, TOP_K = 8, TOP_LIST = 32, TOP_BLOCKS_PER_SM = 4;
 
@@ -584,8 +607,7 @@ __global__ void __launch_bounds__(RL_THREADS, TOP_BLOCKS_PER_SM)
     const int t = in ? t0 + sub : a.T - 1;
     float v[V];
     const bool live = in && (!a.mask || a.mask[t] != 0);
-#pragma unroll
-    for (int h = 0; h < V / 8; ++h) load_row8<BF16>(a.logits, t, E, V / 8 * g + h, vec, v + 8 * h);
+    load_row<BF16, V>(a.logits, t, E, g, vec, v);
     float x = neg_inf();
 #pragma unroll
     for (int i = 0; i < V; ++i) x = fmaxf(x, v[i]);  // passes over NaN
@@ -961,7 +983,7 @@ cudaError_t launch_router_losses(const RouterLossArgs& a, bool bf16, void* ws, c
   // of four experts: 8.4 us, two launches 10.4); more passes take longer than the
   // second launch
   const bool one = a.T <= 2 * RF_CLUSTER * RL_WARPS * (32 / group_width(a.E));
-  const bool top8 = !one && a.k <= TOP_K && (a.E > 128 || (a.E > 64 && a.k >= 3));
+  const bool top8 = !one && a.k <= TOP_K && (a.E > 128 || (a.E > 64 && a.k >= 3) || (a.E > 32 && a.k >= 5));
   const unsigned blocks = one ? RF_CLUSTER : top8 ? top8_blocks(a.T) : loss_blocks(a.T, a.E);
   LossPartials part;
   part.sums = static_cast<float*>(ws);
@@ -970,7 +992,8 @@ cudaError_t launch_router_losses(const RouterLossArgs& a, bool bf16, void* ws, c
   part.n = reinterpret_cast<int32_t*>(part.z + blocks);
   const bool vec = rows_vectorised(a.logits, a.logits, a.E);
   if (top8) {
-    const auto kernel = a.E <= 8 * TOP_LANES ? (bf16 ? router_loss_top8_kernel<true, 8> : router_loss_top8_kernel<false, 8>)
+    const auto kernel = a.E <= 4 * TOP_LANES ? (bf16 ? router_loss_top8_kernel<true, 4> : router_loss_top8_kernel<false, 4>)
+                        : a.E <= 8 * TOP_LANES ? (bf16 ? router_loss_top8_kernel<true, 8> : router_loss_top8_kernel<false, 8>)
                                              : (bf16 ? router_loss_top8_kernel<true, 16> : router_loss_top8_kernel<false, 16>);
     kernel<<<blocks, RL_THREADS, 0, st>>>(a, part, vec);
     count_launch();

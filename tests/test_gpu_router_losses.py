@@ -134,7 +134,7 @@ def test_workload_logits(name):
     _run(z, cfg.k, mask=mask)
 
 
-@pytest.mark.parametrize("E", [65, 72, 100, 128, 129, 136, 200, 256])
+@pytest.mark.parametrize("E", [33, 40, 63, 64, 65, 72, 100, 128, 129, 136, 200, 256])
 @pytest.mark.parametrize("k", [1, 2, 3, 5, 8])
 @pytest.mark.parametrize("bf16", [False, True])
 def test_many_experts_with_few_kept(E, k, bf16):
@@ -142,7 +142,7 @@ def test_many_experts_with_few_kept(E, k, bf16):
     _run(rng.normal(size=(601, E)) * 2 + rng.normal(size=E), k, bf16=bf16, mask=rng.random(601) < 0.9)
 
 
-@pytest.mark.parametrize("E", [96, 250])
+@pytest.mark.parametrize("E", [62, 96, 250])
 @pytest.mark.parametrize("kind", ["all equal", "two values", "five values", "rising", "falling", "one lane", "two lanes",
                                   "minus infinity", "zeros of both signs", "zero rows"])
 def test_many_experts_with_ties(E, kind):
