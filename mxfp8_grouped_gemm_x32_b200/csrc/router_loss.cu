@@ -475,13 +475,12 @@ __global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM<G>)
     }
     __syncwarp();  // the list is read before the next token's is written
     // softmax over all experts (what is no expert holds -inf and adds 0).  The
-    // product m log2(e) is rounded once for all terms: a factor 1 +- 2^-24 |m|
-    // that cancels in s and moves lse by less than its own rounding
+    // difference first: m log2(e) overflows where m is near the type's lowest value
+    // (a row whose experts are all switched off by it) or its largest
     float se = 0.0f;
-    const float ml = m * LOG2E;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      v[i] = fast_exp2(fmaf(v[i], LOG2E, -ml));
+      v[i] = fast_exp2((v[i] - m) * LOG2E);
       se += v[i];
     }
     if (nan) se = __int_as_float(0x7FC00000);
@@ -620,11 +619,10 @@ __global__ void __launch_bounds__(RL_THREADS, TOP_BLOCKS_PER_SM)
       }
     const float m = __shfl_sync(0xFFFFFFFFu, x, 0, G), least = __shfl_sync(0xFFFFFFFFu, x, k - 1, G);
     // softmax over all experts, as in the kernel above
-    const float ml = m * LOG2E;
     float ex[V], se = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      ex[i] = fast_exp2(fmaf(v[i], LOG2E, -ml));
+      ex[i] = fast_exp2((v[i] - m) * LOG2E);
       se += ex[i];
     }
     if (se != se) {  // NaN (or infinities) among the lane's logits
@@ -869,15 +867,21 @@ __global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM<G>)
       id[j] = id_next[j];
     }
     if (t0 + step < a.T) fetch(t0 + step);
-    float fs = 0.0f;
+    // s up to a factor that lse's rounding leaves (up to e^4 at 1e8, E where log E is lost in
+    // it), hence the division by their sum
+    float fs = 0.0f, one = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      d[i] = fast_exp2((d[i] - lse) * LOG2E);  // s (0 where there is no expert)
+      d[i] = fast_exp2((d[i] - lse) * LOG2E);  // 0 where there is no expert
+      one += d[i];
       fs = fmaf(d[i], f[i], fs);
     }
+    one = group_sum<G>(one);
     fs = group_sum<G>(fs);
+    const float inv = __fdividef(1.0f, one), cbs = cb * inv, czs = cz * lse * inv;
+    fs *= inv;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) d[i] *= fmaf(cb, f[i] - fs, cz * lse);
+    for (int i = 0; i < 8; ++i) d[i] *= fmaf(cbs, f[i] - fs, czs);
     if (a.dprob) {
       float dot = 0.0f;
 #pragma unroll

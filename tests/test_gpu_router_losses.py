@@ -230,6 +230,63 @@ def test_minus_infinity_logits():
     _run(z, 4)
 
 
+@pytest.mark.parametrize("E,k", [(12, 4), (48, 6), (128, 2), (200, 8), (256, 20)])
+def test_rows_of_the_lowest_value_and_huge_logits(E, k):
+    """Rows whose experts are all switched off by the type's lowest value are
+    rows of equal logits; the softmax holds at any magnitude."""
+    import torch
+    rng = np.random.default_rng(E)
+    T = 700
+    low = -3.4028234663852886e38
+    z = rng.normal(size=(T, E)).astype(np.float32)
+    z[0::7] = low
+    z[1::7, E // 2:] = low
+    z[2::7] *= np.float32(3e37)
+    z[3::7] = np.float32(3.4e38)
+    z[4::7] += np.float32(1e8)
+    z[5::7] -= np.float32(3e5)
+    layer = _layer(T, E, k)
+    dz = _device(z)
+    idx, prob, losses = layer.route_losses(dz)
+    dp = rng.normal(size=(T, k)).astype(np.float32)
+    g = layer.route_backward(dz, torch.from_numpy(dp).cuda(), torch.tensor([0.3, 0.0], device="cuda"))
+    f = orouter.route_losses(z, k)
+    assert np.array_equal(idx.cpu().numpy(), f["idx"])
+    assert np.array_equal(layer.expert_counts.cpu().numpy(), f["counts"])
+    gp = prob.cpu().numpy().astype(np.float64)
+    assert np.all(np.abs(gp - f["prob"]) <= 4e-6 * f["prob"] + 1e-30)
+    lse = layer.router_lse.cpu().numpy().astype(np.float64)
+    assert np.all(np.abs(lse - f["lse"]) <= 6e-6 + 2.0 ** -23 * np.abs(f["lse"]))
+    assert np.all(np.abs(layer.prob_sums.cpu().numpy() - f["sums"]) <= 1e-5 * f["sums"] + 1e-30)
+    assert abs(float(losses[0]) - f["losses"][0]) <= 2e-5 * f["losses"][0]
+    assert float(losses[1]) == np.inf                # the square passes fp32
+    ref, bar = _grad_bar(f, E, dp, np.array([np.float32(0.3), 0.0], np.float64), False)
+    got = g.cpu().numpy().astype(np.float64)
+    assert np.all(np.abs(got - ref) <= bar), float(np.max(np.abs(got - ref) - bar))
+
+
+@pytest.mark.parametrize("E,k", [(48, 6), (100, 4), (200, 8)])
+def test_nan_and_infinity_among_many_experts(E, k):
+    import torch
+    rng = np.random.default_rng(E)
+    T = 640
+    z = rng.normal(size=(T, E)).astype(np.float32)
+    z[3, 4], z[9, 0], z[20], z[33, ::2] = np.nan, np.inf, -np.inf, np.nan
+    layer = _layer(T, E, k)
+    dz = _device(z)
+    idx, prob, losses = layer.route_losses(dz)
+    g = layer.route_backward(dz, torch.ones(T, k, device="cuda"), torch.ones(2, device="cuda"))
+    idx, prob = idx.clone(), prob.clone()
+    i2, p2 = layer.route(dz)
+    f = orouter.route_losses(z, k)
+    assert np.array_equal(idx.cpu().numpy(), f["idx"]) and torch.equal(idx, i2)
+    assert torch.equal(prob.view(torch.int32)[~torch.isnan(prob)], p2.view(torch.int32)[~torch.isnan(p2)])
+    assert torch.isnan(losses).all()
+    clean = torch.ones(T, dtype=torch.bool, device="cuda")
+    clean[[3, 9, 20, 33]] = False
+    assert torch.isfinite(g[clean]).all() and torch.isnan(g[~clean]).any(1).all()
+
+
 def test_nan_and_infinity_stay_in_their_tokens():
     import torch
     rng = np.random.default_rng(12)
