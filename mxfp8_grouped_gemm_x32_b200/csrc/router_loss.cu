@@ -34,7 +34,7 @@ constexpr int RL_WARPS = RL_THREADS / 32;
 // Wide rows (groups of 16 or 32 lanes): four blocks per SM, a token's logits loaded
 // when they are needed.  Narrow ones: three, with the next token's logits on their
 // way -- more kept experts per lane need more registers (gradient of 262144 x 256:
-// 109 against 125 us, x 32: 45 against 41).
+// 109 against 125 us, x 32: 45 against 41, now 113 and 37).
 template <int G>
 constexpr bool RL_WIDE = G >= 16;
 template <int G>
