@@ -225,6 +225,7 @@ __device__ __forceinline__ void epilogue_tile4(const Gemm4Args& a, const CUtenso
     uint8_t* sfr = a.sf_out + sf_offset(0, r, 0, 0, (N + 127) / 128);
 #pragma unroll 1
     for (int b = 0; b < blocks; ++b) {
+      __syncwarp();  // lanes without a token skip the arithmetic; the whole warp reads TMEM
       uint32_t g[32], u[32];
       tmem_ld32(tl + 32 * b, g);
       tmem_ld32(tl + 96 + 32 * b, u);
@@ -257,6 +258,7 @@ __device__ __forceinline__ void epilogue_tile4(const Gemm4Args& a, const CUtenso
     const bool any = ti.m0 + 32 * q < ti.row_end;
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
+      __syncwarp();  // lane 0 issues the stores; the whole warp reads TMEM
       uint32_t v[32];
       tmem_ld32(tl + 32 * c, v);
       tc_wait_ld();
@@ -373,6 +375,7 @@ __global__ void __launch_bounds__(Cfg4<EPI>::THREADS, 1)
         if (lane == 0) mbar_arrive(&sf_empty[slot]);
         if (++slot == C::SF_RING) { slot = 0; slot_phase ^= 1u; }
         if (lane == 0) landed = mbar_test_wait(&sf_loaded[slot], slot_phase);
+        __syncwarp();  // the wait is the whole warp's
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
