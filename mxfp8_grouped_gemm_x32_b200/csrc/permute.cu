@@ -38,6 +38,7 @@ __global__ void __launch_bounds__(PB) perm_hist_kernel(const int32_t* __restrict
       set_status(MOE_ERR_DEVICE_INDEX);
   }
   __syncthreads();
+  if (R == 0) return;  // an empty batch: no block of slots, and no room for its counts in the workspace
   for (int i = threadIdx.x; i < E; i += PB) hist[int64_t(blockIdx.x) * E + i] = cnt[i];
 }
 
