@@ -139,8 +139,10 @@ class GroupedMLP:
         self.group_offsets = al.typed((E + 1,), torch.int32, "group_offsets")
         self.row_to_slot = al.typed((rc,), torch.int32, "row_to_slot")
         self.slot_to_row = al.typed((T * k,), torch.int32, "slot_to_row")
-        self.topk_idx = al.typed((T, k), torch.int32, "topk_idx")        # router outputs
-        self.topk_prob = al.typed((T, k), torch.float32, "topk_prob")
+        # router outputs: topk_idx and topk_prob are those of the last routing
+        # call; route_losses has its own (kept for route_backward)
+        self._routed = (al.typed((T, k), torch.int32, "topk_idx"), al.typed((T, k), torch.float32, "topk_prob"))
+        self.topk_idx, self.topk_prob = self._routed
         self.prob_perm = al.typed((rc,), torch.float32, "prob_perm")
         if mxfp8:
             self.xq = u8(rc * H, "xq")
@@ -172,7 +174,8 @@ class GroupedMLP:
             self.saved_a = None
         self.xq_col = self.xq_col_sf = None   # x along tokens: only when permute(..., with_cols=True)
         self._x = None                         # the input of the last permutation (the backward's x)
-        self.router_lse = None                 # route_losses' outputs, once it has run
+        self.router_lse = None                 # route_losses' outputs and mask, once it has run
+        self._loss_mask = None
         self.dlogits = {}                      # route_backward's, one buffer per type it has met
         self.w1q4 = None                       # MXFP4 weights, once quantised or loaded
 
@@ -294,7 +297,8 @@ class GroupedMLP:
         z-loss), in this layer's buffers; the tokens per expert land in
         self.expert_counts (int32 [E]), the sums of the experts' softmax
         probabilities in self.prob_sums (fp32 [E]), the number of unmasked
-        tokens in self.routed_tokens (int32 [1]).  For a loss over a
+        tokens in self.routed_tokens (int32 [1]).  All of it, ids and
+        probabilities too, stays until the next route_losses.  For a loss over a
         data-parallel job's whole batch, add the counts and tokens up over the
         ranks before route_backward."""
         T, E, k = self.T, self.E, self.k
@@ -304,6 +308,8 @@ class GroupedMLP:
             check_tensor(token_mask, "token_mask", torch.bool, (T,), self.dev)
         if self.router_lse is None:
             al = self._alloc
+            self._loss_idx = al.typed((T, k), torch.int32, "loss_topk_idx")
+            self._loss_prob = al.typed((T, k), torch.float32, "loss_topk_prob")
             self.router_lse = al.typed((T,), torch.float32, "router_lse")
             self.expert_counts = al.typed((E,), torch.int32, "expert_counts")
             self.prob_sums = al.typed((E,), torch.float32, "prob_sums")
@@ -312,18 +318,22 @@ class GroupedMLP:
             self.ws_losses_bytes = lib.moe_workspace_size(lib.MOE_OP_ROUTER_LOSSES, T, k, E, 0, 0)
             self.ws_losses = al.raw(self.ws_losses_bytes, "ws_losses")
         with on_device(self.dev):
-            lib.moe_router_losses(logits.data_ptr(), dt, T, E, k, _ptr(token_mask), _ptr(self.topk_idx),
-                                  _ptr(self.topk_prob), _ptr(self.router_lse), _ptr(self.expert_counts),
+            lib.moe_router_losses(logits.data_ptr(), dt, T, E, k, _ptr(token_mask), _ptr(self._loss_idx),
+                                  _ptr(self._loss_prob), _ptr(self.router_lse), _ptr(self.expert_counts),
                                   _ptr(self.prob_sums), _ptr(self.routed_tokens), _ptr(self.router_losses),
                                   _ptr(self.ws_losses), self.ws_losses_bytes, self._stream())
+        self._loss_mask = token_mask
+        self.topk_idx, self.topk_prob = self._loss_idx, self._loss_prob
         return self.topk_idx, self.topk_prob, self.router_losses
 
     def route_backward(self, logits: torch.Tensor, dprob: torch.Tensor = None, dlosses: torch.Tensor = None,
                        token_mask: torch.Tensor = None) -> torch.Tensor:
         """Gradient of the logits (moe_router_bwd) after route_losses on the
-        same logits and mask: dprob fp32 [T, k] (as backward() returns it)
-        and dlosses fp32 [2], either None for zero -> dlogits [T, E] in the
-        logits' type, in a buffer of this layer (one per type)."""
+        same logits and mask (other routing calls may have come in between;
+        token_mask None: the tensor that route_losses was given): dprob fp32
+        [T, k] (as backward() returns it) and dlosses fp32 [2], either None for
+        zero -> dlogits [T, E] in the logits' type, in a buffer of this layer
+        (one per type)."""
         T, E, k = self.T, self.E, self.k
         dt = _logits_dtype(logits)
         check_tensor(logits, "logits", logits.dtype, (T, E), self.dev)
@@ -335,12 +345,14 @@ class GroupedMLP:
             check_tensor(dlosses, "dlosses", torch.float32, (2,), self.dev)
         if token_mask is not None:
             check_tensor(token_mask, "token_mask", torch.bool, (T,), self.dev)
+        else:
+            token_mask = self._loss_mask
         if logits.dtype not in self.dlogits:
             self.dlogits[logits.dtype] = self._alloc.typed((T, E), logits.dtype, "dlogits")
         dlogits = self.dlogits[logits.dtype]
         with on_device(self.dev):
-            lib.moe_router_bwd(logits.data_ptr(), dt, T, E, k, _ptr(token_mask), _ptr(self.topk_idx),
-                               _ptr(self.topk_prob), _ptr(self.router_lse), _ptr(self.expert_counts),
+            lib.moe_router_bwd(logits.data_ptr(), dt, T, E, k, _ptr(token_mask), _ptr(self._loss_idx),
+                               _ptr(self._loss_prob), _ptr(self.router_lse), _ptr(self.expert_counts),
                                _ptr(self.routed_tokens), _ptr(dprob), _ptr(dlosses), _ptr(dlogits), self._stream())
         return dlogits
 
@@ -440,6 +452,7 @@ class GroupedMLP:
         if dt is None:
             raise TypeError(f"logits: expected float32 or bfloat16, got {logits.dtype}")
         check_tensor(logits, "logits", logits.dtype, (self.T, self.E), self.dev)
+        self.topk_idx, self.topk_prob = self._routed
         lib.moe_router_topk(logits.data_ptr(), dt, self.T, self.E, self.k, _ptr(self.topk_idx),
                             _ptr(self.topk_prob), self._stream())
         return self.topk_idx, self.topk_prob
@@ -455,6 +468,7 @@ class GroupedMLP:
         check_tensor(logits, "logits", logits.dtype, (self.T, self.E), self.dev)
         check_tensor(x, "x", torch.bfloat16, (self.T, self.H), self.dev)
         xc, xcs = self._cols(with_cols)
+        self.topk_idx, self.topk_prob = self._routed
         lib.moe_route_permute(logits.data_ptr(), dt, x.data_ptr(), self.T, self.H, self.k, self.E, self.rows_cap,
                               _ptr(self.topk_idx), _ptr(self.topk_prob), _ptr(self.split_sizes),
                               _ptr(self.group_offsets), _ptr(self.row_to_slot), _ptr(self.slot_to_row),
