@@ -28,6 +28,7 @@ Steps (names of the C entry points):
 from __future__ import annotations
 
 import contextlib
+import functools
 
 import torch
 
@@ -103,6 +104,15 @@ def on_device(dev: torch.device):
     """Context in which `dev` is the current device (the library launches on
     the current device; nothing to do when it already is)."""
     return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _on_layer_device(call):
+    """A method that runs with its layer's device current."""
+    @functools.wraps(call)
+    def wrapped(self, *args, **kwargs):
+        with on_device(self.dev):
+            return call(self, *args, **kwargs)
+    return wrapped
 
 
 # the raw handle of a device's current stream; the public call builds a Stream
@@ -204,6 +214,7 @@ class GroupedMLP:
                             _ptr(self.slot_to_row), _ptr(self.prob_perm), 0, 0, 0, 0, _ptr(self.ws_perm),
                             self.ws_perm_bytes, self._stream())
 
+    @_on_layer_device
     def forward_bf16(self, x: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor) -> torch.Tensor:
         """BF16 recipe forward (moe_grouped_mlp_fwd_bf16) on the routing of
         the last permute / permute_index: x bf16 [T, H], w1 bf16 [E, 2I, H],
@@ -221,6 +232,7 @@ class GroupedMLP:
                                      _ptr(self.saved_a), _ptr(self.ws_bf16), self.ws_bf16_bytes, self._stream())
         return self.out
 
+    @_on_layer_device
     def backward_bf16(self, dY: torch.Tensor, x: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor):
         """BF16 recipe backward (moe_grouped_mlp_bwd_bf16) after forward_bf16
         on the same routing: dY, x bf16 [T, H], w1 bf16 [E, 2I, H], w2 bf16
@@ -243,6 +255,7 @@ class GroupedMLP:
                                      self.ws_bwd_bf16_bytes, self._stream())
         return self.dX, self.dW1, self.dW2, self.dprob
 
+    @_on_layer_device
     def forward_fp8_tensor(self, x: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor) -> torch.Tensor:
         """Per-tensor FP8 recipe forward (moe_grouped_mlp_fwd_fp8_tensor) on
         the routing of the last permute / permute_index: x bf16 [T, H], w1
@@ -263,6 +276,7 @@ class GroupedMLP:
                                            _ptr(self.ws_f8t), self.ws_f8t_bytes, self._stream())
         return self.out
 
+    @_on_layer_device
     def backward_fp8_tensor(self, dY: torch.Tensor, x: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor):
         """Per-tensor FP8 recipe backward (moe_grouped_mlp_bwd_fp8_tensor)
         after forward_fp8_tensor on the same routing, x and weights -> (dX,
@@ -430,6 +444,7 @@ class GroupedMLP:
     def _stream(self) -> int:
         return _raw_stream(self.dev.index)
 
+    @_on_layer_device
     def quantize_weights(self, w1: torch.Tensor, w2: torch.Tensor) -> None:
         """w1 bf16 [E, 2I, H] (gate rows first), w2 bf16 [E, H, I]."""
         self._need_mxfp8()
@@ -445,6 +460,7 @@ class GroupedMLP:
         lib.moe_mlp_quantize_mxfp8(w1.data_ptr(), 2 * E, I, H, lib.MOE_QUANT_ROW, _ptr(self.w1q), _ptr(self.w1sf), s)
         lib.moe_mlp_quantize_mxfp8(w2.data_ptr(), E, H, I, lib.MOE_QUANT_ROW, _ptr(self.w2q), _ptr(self.w2sf), s)
 
+    @_on_layer_device
     def route(self, logits: torch.Tensor):
         """Router logits fp32 or bf16 [T, E] -> (topk_idx int32 [T, k],
         topk_prob float32 [T, k]) in this layer's routing buffers."""
@@ -457,6 +473,7 @@ class GroupedMLP:
                             _ptr(self.topk_prob), self._stream())
         return self.topk_idx, self.topk_prob
 
+    @_on_layer_device
     def route_permute(self, logits: torch.Tensor, x: torch.Tensor, with_cols: bool = False):
         """Router and permutation in one call (moe_route_permute): logits fp32
         or bf16 [T, E], x bf16 [T, H]; the routing lands in topk_idx /
@@ -477,6 +494,7 @@ class GroupedMLP:
         self._x = x
         return self.topk_idx, self.topk_prob
 
+    @_on_layer_device
     def permute(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_prob: torch.Tensor,
                 with_cols: bool = False) -> None:
         """x bf16 [T, H]; topk_idx int32 [T, k]; topk_prob float32 [T, k].
@@ -494,6 +512,7 @@ class GroupedMLP:
                         self._stream())
         self._x = x
 
+    @_on_layer_device
     def forward(self) -> torch.Tensor:
         self._need_mxfp8()
         lib.moe_grouped_mlp_fwd(_ptr(self.w1q), _ptr(self.w1sf), _ptr(self.w2q), _ptr(self.w2sf), self.T,
@@ -505,6 +524,7 @@ class GroupedMLP:
                                 self._stream())
         return self.out
 
+    @_on_layer_device
     def backward(self, dY: torch.Tensor, x: torch.Tensor = None):
         """dY bf16 [T, H]; x defaults to the input of the last permutation."""
         self._need_mxfp8()
@@ -534,5 +554,6 @@ class GroupedMLP:
             return out
         return (out,) + tuple(self.backward(dY, x))
 
+    @_on_layer_device
     def device_status(self) -> int:
         return lib.moe_get_device_status(self._stream())
