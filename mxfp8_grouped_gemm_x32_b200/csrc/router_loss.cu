@@ -56,6 +56,12 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// Squares of lse are summed as (2^-16 lse)^2: fewer than 2^30 of them pass fp32 only
+// where their mean does, and only a |lse| below 2^-47 loses bits.  The finishing
+// cluster undoes the factor in 64 bits.
+constexpr float Z_SCALE = 1.0f / 65536.0f;
+constexpr double Z_UNSCALE = 65536.0 * 65536.0;
+
 // Experts 8g..8g+7 of row t; experts past E read as -inf.  `vec`: rows start
 // on 16-byte boundaries and E is a multiple of 8.
 template <bool BF16>
@@ -230,7 +236,7 @@ __device__ __forceinline__ Best best_unused(const float* v, uint32_t used, uint3
 struct LossPartials {
   float* sums;      // [blocks][E]
   int32_t* counts;  // [blocks][E]
-  float* z;         // [blocks]
+  float* z;         // [blocks], squares scaled (Z_SCALE)
   int32_t* n;       // [blocks]
 };
 
@@ -340,7 +346,7 @@ __device__ __forceinline__ void finish_losses(const RouterLossArgs& a, const Los
       }
       *a.tokens = int32_t(n);
       a.losses[0] = n > 0.0 ? float(double(a.E) * dot / (n * n * double(a.k))) : 0.0f;
-      a.losses[1] = n > 0.0 ? float(z / n) : 0.0f;
+      a.losses[1] = n > 0.0 ? float(z * Z_UNSCALE / n) : 0.0f;
     }
   }
   cluster_sync_all();  // no block leaves while its shared memory is read
@@ -485,7 +491,7 @@ __global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM<G>)
     }
     if (nan) se = __int_as_float(0x7FC00000);
     se = group_sum<G>(se);
-    const float lse = live ? m + __logf(se) : 0.0f;  // se >= 1: 2^-21 absolute
+    const float lse = live ? m + __logf(se) : 0.0f;  // 3 ulp of log(se) <= log(256): 2^-19.4 absolute
     if (in && g == 0) a.lse[t] = lse;
     if (live) {
       const float inv = __fdividef(1.0f, se);
@@ -496,7 +502,7 @@ __global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM<G>)
       cnt_lo += ((kept & 15u) * 0x00204081u) & 0x01010101u;
       cnt_hi += ((kept >> 4) * 0x00204081u) & 0x01010101u;
       if (g == 0) {
-        zsum += lse * lse;
+        zsum = fmaf(Z_SCALE * lse, Z_SCALE * lse, zsum);
         n += 1;
       }
     }
@@ -638,7 +644,7 @@ __global__ void __launch_bounds__(RL_THREADS, TOP_BLOCKS_PER_SM)
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[i] = fmaf(ex[i], inv, acc[i]);
       if (g == 0) {
-        zsum += lse * lse;
+        zsum = fmaf(Z_SCALE * lse, Z_SCALE * lse, zsum);
         n += 1;
       }
     }
