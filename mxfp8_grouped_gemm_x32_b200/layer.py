@@ -188,6 +188,7 @@ class GroupedMLP:
         self._loss_mask = None
         self.dlogits = {}                      # route_backward's, one buffer per type it has met
         self.w1q4 = None                       # MXFP4 weights, once quantised or loaded
+        self._permuted = False                 # whether the routing buffers hold a permutation
 
     def _need_mxfp8(self):
         if not self.mxfp8:
@@ -213,6 +214,7 @@ class GroupedMLP:
                             self.rows_cap, _ptr(self.split_sizes), _ptr(self.group_offsets), _ptr(self.row_to_slot),
                             _ptr(self.slot_to_row), _ptr(self.prob_perm), 0, 0, 0, 0, _ptr(self.ws_perm),
                             self.ws_perm_bytes, self._stream())
+        self._permuted = True
 
     @_on_layer_device
     def forward_bf16(self, x: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor) -> torch.Tensor:
@@ -425,6 +427,8 @@ class GroupedMLP:
         if self.w1q4 is None:
             raise RuntimeError("forward_mxfp4 needs quantize_weights_mxfp4 or load_weights_mxfp4 first")
         check_tensor(x, "x", torch.bfloat16, (self.T, H), self.dev)
+        if not self._permuted:
+            raise RuntimeError("forward_mxfp4 needs permute_index, permute or route_permute first")
         if getattr(self, "ws_mxfp4", None) is None:
             self.ws_mxfp4_bytes = lib.moe_workspace_size(lib.MOE_OP_FWD_MXFP4, self.T, self.k, E, H, I)
             self.ws_mxfp4 = self._alloc.raw(self.ws_mxfp4_bytes, "ws_mxfp4")
@@ -491,7 +495,7 @@ class GroupedMLP:
                               _ptr(self.group_offsets), _ptr(self.row_to_slot), _ptr(self.slot_to_row),
                               _ptr(self.prob_perm), _ptr(self.xq), _ptr(self.xq_sf), xc, xcs, _ptr(self.ws_perm),
                               self.ws_perm_bytes, self._stream())
-        self._x = x
+        self._x, self._permuted = x, True
         return self.topk_idx, self.topk_prob
 
     @_on_layer_device
@@ -510,7 +514,7 @@ class GroupedMLP:
                         _ptr(self.row_to_slot), _ptr(self.slot_to_row), _ptr(self.prob_perm),
                         _ptr(self.xq), _ptr(self.xq_sf), xc, xcs, _ptr(self.ws_perm), self.ws_perm_bytes,
                         self._stream())
-        self._x = x
+        self._x, self._permuted = x, True
 
     @_on_layer_device
     def forward(self) -> torch.Tensor:

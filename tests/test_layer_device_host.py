@@ -72,3 +72,26 @@ def test_launches_on_the_layers_device(recorded, name, backward):
     assert recorded
     assert all(dev == L.dev for _, dev, _ in recorded), recorded
     assert all(stream == 99 for _, _, stream in recorded), recorded
+
+
+def test_forward_mxfp4_needs_a_permutation(recorded):
+    """Without one the row maps hold whatever the memory held, and the kernels would read by it."""
+    t = _tensors()
+    L = layer_module.GroupedMLP(T, H, I, E, k, device="cpu", backward=False, mxfp8=False)
+    L.load_weights_mxfp4(t["c1"], t["s1"], t["c2"], t["s2"])
+    recorded.clear()
+    with pytest.raises(RuntimeError, match="permute"):
+        L.forward_mxfp4(t["x"])
+    assert recorded == []
+    L.route(t["z"])
+    with pytest.raises(RuntimeError, match="permute"):
+        L.forward_mxfp4(t["x"])
+    L.permute_index(t["idx"], t["prob"])
+    L.forward_mxfp4(t["x"])
+    assert recorded[-1][0] == "moe_grouped_mlp_fwd_mxfp4"
+    for permute in ("permute", "route_permute"):
+        L = layer_module.GroupedMLP(T, H, I, E, k, device="cpu", backward=False)
+        L.load_weights_mxfp4(t["c1"], t["s1"], t["c2"], t["s2"])
+        CALLS[permute](L, t)
+        L.forward_mxfp4(t["x"])
+        assert recorded[-1][0] == "moe_grouped_mlp_fwd_mxfp4"
