@@ -157,3 +157,23 @@ def test_many_experts(T, E, k):
     torch.cuda.synchronize()
     assert mx._status() == 0 and layer.check_guards() == []
     mx._check_out(out, x, w1, w2, idx, prob)
+
+
+@pytest.mark.parametrize("T,Hd,Id,E,k", [(3, 96, 64, 4, 2), (150, 288, 192, 7, 3), (1200, 416, 832, 5, 2)])
+@pytest.mark.parametrize("byte", [0x00, 0x7F, 0xFF])
+def test_what_the_buffers_held_before(T, Hd, Id, E, k, byte):
+    """The workspace's and the row maps' earlier bytes (NaN scales, largest codes, ids) reach no output."""
+    import torch
+    x, w1, w2, idx, prob = mx._problem(T, Hd, Id, E, k, seed=T)
+    outs = []
+    for fill in (0x55, byte):
+        layer = mx._layer(T, Hd, Id, E, k, w1, w2)
+        layer.permute_index(torch.from_numpy(idx).cuda(), torch.from_numpy(prob).cuda())
+        layer.forward_mxfp4(mx._bf(x))
+        for t in (layer.ws_mxfp4, layer.ws_perm, layer.split_sizes, layer.group_offsets, layer.row_to_slot,
+                  layer.slot_to_row, layer.prob_perm, layer.out):
+            t.view(torch.uint8).fill_(fill)
+        layer.permute_index(torch.from_numpy(idx).cuda(), torch.from_numpy(prob).cuda())
+        outs.append(layer.forward_mxfp4(mx._bf(x)).clone())
+        assert layer.check_guards() == []
+    assert torch.equal(outs[0], outs[1]) and mx._status() == 0
