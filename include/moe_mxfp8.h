@@ -426,7 +426,8 @@ moe_status_t moe_route_permute(const void* logits, int32_t logits_dtype, const v
  *               int32 [1] = n; losses float [2].
  *   workspace   >= moe_workspace_size(MOE_OP_ROUTER_LOSSES, T, k, E, 0, 0).
  * NaN logits rank as -inf in the selection; an unmasked token with a NaN or
- * +inf logit, or with all of them -inf, makes the losses NaN.  Sums run in a
+ * +inf logit, or with all of them -inf, makes the losses NaN; the z-loss is
+ * infinite only where the mean of the squares passes fp32.  Sums run in a
  * fixed order (the same inputs give the same bits).
  * E <= MOE_MAX_EXPERTS, k <= min(E, 32), T*k < 2^30; arrays aligned to their
  * elements, the workspace to 16 bytes. */

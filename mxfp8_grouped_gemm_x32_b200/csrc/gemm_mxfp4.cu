@@ -232,6 +232,10 @@ __device__ __forceinline__ void epilogue_tile4(const Gemm4Args& a, const CUtenso
       tc_wait_ld();
       if (b + 1 == blocks) done();
       if (!rv) continue;
+      // fast exponential and division, 2^-19 relative together for |gate| below 8: with
+      // expf and `/` the kernel takes 869 us instead of 770 (Mixtral), 379 instead of 239
+      // (8191 x 2880, k 4), 99 instead of 73 (4096 x 2048, k 8), while a code of h, next to a border
+      // between two, comes out as the other neighbour in 3 of 8191 and 6 of 8192 tokens
       float h[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
@@ -253,7 +257,9 @@ __device__ __forceinline__ void epilogue_tile4(const Gemm4Args& a, const CUtenso
   } else {
     // 32 columns at a time: 96 bytes a row into the warp's staging buffer and out
     // by a TMA store of 32 rows (rows past the group's last token are padding
-    // rows of the same group; what they hold is never read)
+    // rows of the same group; what they hold is never read).  Dropping the sums'
+    // low eight bits saves a quarter of the rows' bytes and moves a value by less than
+    // 2^-15, 1 / 128 of half a step of the bf16 output
     const int chunks = min(6, (N - ti.n0) >> 5);
     const bool any = ti.m0 + 32 * q < ti.row_end;
 #pragma unroll 1

@@ -34,7 +34,10 @@ constexpr int RL_WARPS = RL_THREADS / 32;
 // Wide rows (groups of 16 or 32 lanes): four blocks per SM, a token's logits loaded
 // when they are needed.  Narrow ones: three, with the next token's logits on their
 // way -- more kept experts per lane need more registers (gradient of 262144 x 256:
-// 109 against 125 us, x 32: 45 against 41, now 113 and 37).
+// 109 against 125 us, x 32: 45 against 41, now 112 and 37).  A lane has places for
+// the most experts its group may keep (eight where up to 32 experts share 2 or 4 lanes),
+// whatever k is: the gradient's kernels of those widths spill some 130 bytes at 80
+// registers, the losses' 28.
 template <int G>
 constexpr bool RL_WIDE = G >= 16;
 template <int G>
@@ -576,8 +579,16 @@ __global__ void __launch_bounds__(RL_THREADS, RL_BLOCKS_PER_SM<G>)
 // 262144 tokens, this kernel against the one above, us: 256 experts k = 8 114 / 182,
 // k = 4 110 / 142, k = 1 108 / 117; 128 experts k = 8 86 / 135, k = 3 83 / 84, k = 2
 // 82 / 76, k = 1 82 / 70; 64 experts k = 8 72 / 98, k = 6 71 / 78, k = 4 70 / 62 --
-// the work hardly grows with k here, so few kept of few stay with the rounds.  Bound by instruction issue (66 %); three blocks
-// per SM (no spills) or the next row's logits on their way: the same or slower.
+// the work hardly grows with k here, so few kept of few stay with the rounds.  Shorter
+// batches, both launches: 4096 tokens 256 experts k = 8 11.8 / 14.8, k = 1 11.3 / 13.8, 128
+// experts k = 8 10.3 / 11.8, k = 3 9.7 / 10.3, k = 1 9.7 / 10.2, 64 experts k = 8 10.2 / 11.3, k = 4
+// 9.7 / 10.3; 32768 tokens 25.7 / 34.2, 24.1 / 25.6, 19.1 / 26.6, 18.4 / 19.5, 17.9 / 17.4,
+// 16.4 / 21.0, 15.8 / 15.5: the same choice within 1 us.  More than eight kept stay with the rounds:
+// 262144 tokens, 256 experts, k = 9 192, k = 16 287, k = 32 554.
+// 290 warp instructions per token, most of them the selection's (the softmax and its sums need
+// some 60), issued 66 % of the time; the first stalls are loads' and shared memory's
+// latency.  Three blocks per SM (no spills; with four 44 bytes at sixteen experts per lane) or the
+// next row's logits on their way: the same or slower.
 constexpr int TOP_LANES = 16, TOP_K = 8, TOP_LIST = 32, TOP_BLOCKS_PER_SM = 4;
 
 template <bool BF16, int V>

@@ -126,7 +126,12 @@ class GroupedMLP:
 
     mxfp8=False leaves out the buffers of the MXFP8 recipe (quantised weights,
     x and h and its workspaces): a layer that routes and serves in MXFP4, or
-    runs one of the recipes on bf16 weights, does not need them."""
+    runs one of the recipes on bf16 weights, does not need them.
+
+    Results and workspaces are the layer's buffers, overwritten by the next call
+    of the same kind: one stream at a time, and no two captured graphs of one
+    layer replayed at the same time.  Layers beside each other are
+    independent."""
 
     def __init__(self, T: int, H: int, I: int, E: int, k: int, device="cuda", backward: bool = True,
                  guard: int = 0, mxfp8: bool = True):

@@ -31,7 +31,9 @@ def quantize(x: torch.Tensor):
     """x fp32 or bf16 [..., rows, K], K a multiple of 32 -> (codes uint8
     [..., rows, K/2], the even element in the low half of a byte; scales uint8,
     blocked, of lib.moe_mx_scale_bytes(groups, rows, K) bytes, groups the
-    product of the axes before the last two)."""
+    product of the axes before the last two).  Every group's scales fill whole
+    tiles of 128 rows, so [N, 1, K] takes 128 rows of scales per row, eight
+    times its codes' bytes: flatten such a tensor to [N, K] first."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"x: expected a torch.Tensor, got {type(x).__name__}")
     dt = _DTYPES.get(x.dtype)
